@@ -4,8 +4,8 @@ Thin Python binding of libsskip_attn.so (C ABI in include/sskip_attn.h). The
 sskip_* functions below only marshal torch tensors into the C calls of the
 same names, and the conveniences after them only allocate outputs and chain
 those calls: every step of the computation runs in the library, in its CUDA
-kernels or, for the two host-side steps (the calibration's factor selection
-and the Hilbert order), in its C++. There is no CPU fallback; a missing
+kernels or, for the host-side steps (the calibration's factor selection, the
+Hilbert order and the rotation frequencies), in its C++. There is no CPU fallback; a missing
 library is an error.
 
 The method (TensorRT-LLM Skip-Softmax article, "Skip Softmax 的三步走算法"
@@ -35,7 +35,8 @@ EXPORTS = ("sskip_version", "sskip_status_string", "sskip_device_supported",
            "sskip_attn_decode", "sskip_attn_decode_ex", "sskip_attn_decode_crit",
            "sskip_attn_decode_noalloc", "sskip_calibrate_factor", "sskip_hilbert3d_order",
            "sskip_permute_rows", "sskip_attn_step", "sskip_attn_prefill_host",
-           "sskip_attn_decode_host",
+           "sskip_attn_decode_host", "sskip_kv_page_bytes", "sskip_rope_freqs",
+           "sskip_kv_append", "sskip_kv_gather", "sskip_attn_decode_paged",
            "sskip_get_status", "sskip_selftest_watchdog")
 
 # Size of the library's fixed decode scratch (see sskip_attn_decode_noalloc).
@@ -47,6 +48,10 @@ class SSkipError(RuntimeError):
         self.status = status
         super().__init__(f"{what}: {status_string(status)} ({status})")
 
+
+# Formats of the paged cache, and the scalings of the rotation frequencies.
+SSKIP_KV_BF16, SSKIP_KV_INT4 = 0, 1
+ROPE_SCALINGS = ("plain", "linear", "bands", "yarn")
 
 _lib = None
 _lib_debug = None
@@ -115,6 +120,18 @@ def _load(path: str) -> ctypes.CDLL:
                                   [I, I, I, F, F, F, P])
     L.sskip_attn_decode_noalloc.restype = I
     L.sskip_attn_decode_noalloc.argtypes = [P, P, P, P, P, P, I, I, I, I, I, F, F, I, I, P, P]
+    LL = ctypes.c_longlong
+    L.sskip_kv_page_bytes.restype = Z
+    L.sskip_kv_page_bytes.argtypes = [I, I, I, I]
+    L.sskip_rope_freqs.restype = I
+    L.sskip_rope_freqs.argtypes = [I, D, I, D, D, D, D, P, P]
+    L.sskip_kv_append.restype = I
+    L.sskip_kv_append.argtypes = ([P, P, P, LL, LL, LL, P, P, P, P, F, P, I, I, F, P, P, P, I] +
+                                  [P, P, P, I, I, I, I, I, I, I, I, I, P])
+    L.sskip_kv_gather.restype = I
+    L.sskip_kv_gather.argtypes = [P] * 7 + [I] * 8 + [I, P]
+    L.sskip_attn_decode_paged.restype = I
+    L.sskip_attn_decode_paged.argtypes = [P] * 7 + [I] * 8 + [F, F, I, P, Z, P, P, P]
     L.sskip_get_status.restype = I
     L.sskip_get_status.argtypes = [P]
     L.sskip_selftest_watchdog.restype = I
@@ -556,3 +573,215 @@ def sskip_attn_step(*, threshold_scale_factor, sm_scale: float, prefill=None, de
                                Lmax, int(num_splits), _ptr(ws), ws_bytes, _ptr(D.get("count")),
                                Hq, Hkv, d, float(sm_scale), tp, td, _stream(stream))
     _check(rc, "sskip_attn_step")
+
+
+# ------------------------------------------------------------ the paged cache
+def sskip_kv_page_bytes(kv_format: int, Hkv: int, page_size: int, d: int) -> int:
+    return int(lib().sskip_kv_page_bytes(int(kv_format), int(Hkv), int(page_size), int(d)))
+
+
+def sskip_rope_freqs(rot_dim: int, base: float, *, scaling: str = "plain", factor: float = 1.0,
+                     slow_turns: float = 1.0, fast_turns: float = 4.0,
+                     original_len: float = 0.0):
+    """Host int64 numpy [rot_dim // 2] of frequencies in 2^-64 turns (the bits
+    of the C call's uint64 table) and the factor on cosine and sine."""
+    import numpy as np
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {ROPE_SCALINGS}")
+    turns = np.empty(max(int(rot_dim) // 2, 1), np.int64)
+    attn = ctypes.c_double(1.0)
+    rc = lib().sskip_rope_freqs(int(rot_dim), float(base), ROPE_SCALINGS.index(scaling),
+                                float(factor), float(slow_turns), float(fast_turns),
+                                float(original_len), turns.ctypes.data_as(ctypes.c_void_p),
+                                ctypes.byref(attn))
+    _check(rc, "sskip_rope_freqs")
+    return turns, attn.value
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+class _on_device:
+    """The device of a call's tensors, made current for its length, and the
+    stream the call launches on."""
+
+    def __init__(self, device, stream):
+        if device.type != "cuda":
+            raise ValueError("expected CUDA tensors")
+        self.device, self.stream = device, stream
+
+    def __enter__(self):
+        self.before = torch.cuda.current_device()
+        if self.before != self.device.index:
+            torch.cuda.set_device(self.device)
+        if self.stream is None:
+            return torch.cuda.current_stream(self.device).cuda_stream
+        return (self.stream.cuda_stream if hasattr(self.stream, "cuda_stream")
+                else int(self.stream))
+
+    def __exit__(self, *exc):
+        if self.before != self.device.index:
+            torch.cuda.set_device(self.before)
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _pages(k_pages, v_pages, block_table, d):
+    """(format, num_pages, Hkv, page_size, B, max_pages) of a paged cache:
+    bf16 [num_pages, Hkv, page_size, d] or uint8 [num_pages, Hkv,
+    page_size // 16, 10 * d] pages and an int32 [B, max_pages] block table."""
+    if k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype or k_pages.dim() != 4:
+        raise ValueError("k_pages and v_pages must be 4-D and of one shape and dtype")
+    if not (k_pages.is_contiguous() and v_pages.is_contiguous() and block_table.is_contiguous()):
+        raise ValueError("pages and block table must be contiguous")
+    if block_table.dtype != torch.int32 or block_table.dim() != 2:
+        raise TypeError("block_table must be a 2-D int32 tensor")
+    N, Hkv, rows, width = k_pages.shape
+    if k_pages.dtype == torch.uint8:
+        if width != 10 * d:
+            raise ValueError(f"4-bit records of d = {d} hold {10 * d} bytes, got {width}")
+        return SSKIP_KV_INT4, N, Hkv, rows * 16, block_table.shape[0], block_table.shape[1]
+    if k_pages.dtype != torch.bfloat16:
+        raise TypeError(f"pages must be bf16, or uint8 records, got {k_pages.dtype}")
+    if width != d:
+        raise ValueError(f"pages hold rows of {width}, expected d = {d}")
+    return SSKIP_KV_BF16, N, Hkv, rows, block_table.shape[0], block_table.shape[1]
+
+
+def _token_rows(t, what):
+    """[T, H, d] bf16, heads packed, any stride between tokens (one token's
+    stride means nothing)."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{what} must be bf16, got {t.dtype}")
+    T, H, d = t.shape
+    if t.stride(2) != 1 or (H > 1 and t.stride(1) != d):
+        raise ValueError(f"{what}: the heads of a token must be packed")
+    return H * d if T <= 1 else t.stride(0)
+
+
+def _tokens(t, T, what):
+    if t is not None:
+        if t.dtype != torch.int32 or not t.is_contiguous():
+            raise TypeError(f"{what} must be contiguous int32")
+        if t.numel() != T:
+            raise ValueError(f"{what} needs {T} entries")
+    return t
+
+
+def _rows_out(t, T, H, d, what):
+    """out_len of a [T // out_len, H, out_len, d] (or [T, H, d]) output."""
+    if t.dtype != torch.bfloat16 or not t.is_contiguous():
+        raise TypeError(f"{what} must be contiguous bf16")
+    out_len = 1 if t.dim() == 3 else t.shape[2]
+    if t.numel() != T * H * d or t.shape[1] != H or t.shape[-1] != d:
+        raise ValueError(f"{what} must be [T / out_len, {H}, out_len, {d}] with T = {T}")
+    return out_len
+
+
+def sskip_kv_append(q, k, v, seq_ids, positions, *, q_out=None, k_out=None, v_out=None,
+                    k_pages=None, v_pages=None, block_table=None, turns=None,
+                    interleaved: bool = False, attn_factor: float = 1.0, q_weight=None,
+                    k_weight=None, eps: float = 1e-6, stream=None) -> None:
+    """Marshal q [T,Hq,d], k, v [T,Hkv,d] bf16 (q, or k and v, may be None),
+    seq_ids and positions [T] int32, the norm weights [d] bf16, the int64
+    turns table [rot_dim // 2], outputs [T // out_len, H, out_len, d] (or
+    [T, H, d]) and a paged cache into sskip_kv_append."""
+    ref = q if q is not None else k
+    T, _, d = ref.shape
+    Hq = 0 if q is None else q.shape[1]
+    Hkv = 0 if k is None else k.shape[1]
+    if (k is None) != (v is None) or (k is not None and k.shape != v.shape) or \
+            (q is not None and k is not None and (k.shape[0] != T or k.shape[2] != d)):
+        raise ValueError("q, k and v must have one T and d, k and v one shape")
+    dev = ref.device
+    _same_device(dev, q=q, k=k, v=v, seq_ids=seq_ids, positions=positions, q_out=q_out,
+                 k_out=k_out, v_out=v_out, k_pages=k_pages, v_pages=v_pages,
+                 block_table=block_table, turns=turns, q_weight=q_weight, k_weight=k_weight)
+    qs = 0 if q is None else _token_rows(q, "q")
+    ks, vs = (0, 0) if k is None else (_token_rows(k, "k"), _token_rows(v, "v"))
+    _tokens(seq_ids, T, "seq_ids")
+    _tokens(positions, T, "positions")
+    lens = {_rows_out(t, T, H, d, n) for t, H, n in ((q_out, Hq, "q_out"), (k_out, Hkv, "k_out"),
+                                                     (v_out, Hkv, "v_out")) if t is not None}
+    if len(lens) > 1:
+        raise ValueError("q_out, k_out and v_out must share one layout")
+    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None and (w.dtype != torch.bfloat16 or not w.is_contiguous() or
+                              w.numel() != d):
+            raise TypeError(f"{n} must be contiguous bf16 of {d} values")
+    if turns is not None and (turns.dtype != torch.int64 or not turns.is_contiguous()):
+        raise TypeError("turns must be contiguous int64")
+    fmt = N = P = B = M = 0
+    if k_pages is not None or v_pages is not None:
+        if k_pages is None or v_pages is None or block_table is None:
+            raise ValueError("a cache needs k_pages, v_pages and block_table")
+        fmt, N, heads, P, B, M = _pages(k_pages, v_pages, block_table, d)
+        if heads != Hkv:
+            raise ValueError(f"the pages hold {heads} heads, k and v {Hkv}")
+    with _on_device(dev, stream) as st:
+        rc = lib().sskip_kv_append(
+            _addr(q), _addr(k), _addr(v), qs, ks, vs, _addr(seq_ids), _addr(positions),
+            _addr(q_weight), _addr(k_weight), eps, _addr(turns),
+            0 if turns is None else 2 * turns.numel(), int(bool(interleaved)), attn_factor,
+            _addr(q_out), _addr(k_out), _addr(v_out), max(lens) if lens else 1, _addr(k_pages),
+            _addr(v_pages), _addr(block_table), fmt, N, P, M, T, B, Hq, Hkv, d, st)
+    _check(rc, "sskip_kv_append")
+
+
+def sskip_kv_gather(k_pages, v_pages, block_table, seq_ids, positions, k_out, v_out, *,
+                    stream=None) -> None:
+    """Marshal a paged cache, seq_ids and positions [T] int32 and bf16 outputs
+    [T // out_len, Hkv, out_len, d] (or [T, Hkv, d]) into sskip_kv_gather."""
+    dev, d, T = k_pages.device, k_out.shape[-1], seq_ids.numel()
+    _same_device(dev, v_pages=v_pages, block_table=block_table, seq_ids=seq_ids,
+                 positions=positions, k_out=k_out, v_out=v_out)
+    fmt, N, Hkv, P, B, M = _pages(k_pages, v_pages, block_table, d)
+    _tokens(seq_ids, T, "seq_ids")
+    _tokens(positions, T, "positions")
+    out_len = _rows_out(k_out, T, Hkv, d, "k_out")
+    if _rows_out(v_out, T, Hkv, d, "v_out") != out_len:
+        raise ValueError("k_out and v_out must share one layout")
+    with _on_device(dev, stream) as st:
+        rc = lib().sskip_kv_gather(_addr(k_pages), _addr(v_pages), _addr(block_table),
+                                   _addr(seq_ids), _addr(positions), _addr(k_out), _addr(v_out),
+                                   out_len, fmt, N, P, M, T, B, Hkv, d, st)
+    _check(rc, "sskip_kv_gather")
+
+
+def sskip_attn_decode_paged(q, k_pages, v_pages, block_table, seqlens, o, lse, *, sm_scale: float,
+                            threshold_scale_factor: float, num_splits: int = 16, workspace=None,
+                            skip_count=None, tile_state=None, stream=None) -> None:
+    """Marshal q [B,Hq,d] bf16, a paged cache, seqlens [B] int32, o [B,Hq,d]
+    bf16, lse [B,Hq] fp32 and a uint8 workspace into sskip_attn_decode_paged."""
+    dev = q.device
+    _same_device(dev, k_pages=k_pages, v_pages=v_pages, block_table=block_table, seqlens=seqlens,
+                 o=o, lse=lse, workspace=workspace, skip_count=skip_count, tile_state=tile_state)
+    B, Hq, d = q.shape
+    fmt, N, Hkv, P, rows, M = _pages(k_pages, v_pages, block_table, d)
+    if q.dtype != torch.bfloat16 or o.dtype != torch.bfloat16:
+        raise TypeError("q and o must be bf16")
+    if not (q.is_contiguous() and o.is_contiguous() and lse.is_contiguous()):
+        raise ValueError("tensors must be contiguous")
+    if o.shape != q.shape or lse.numel() != B * Hq or rows != B:
+        raise ValueError("q, o, lse and block_table must belong to one batch")
+    if lse.dtype != torch.float32:
+        raise TypeError(f"lse must be float32, got {lse.dtype}")
+    _tokens(seqlens, B, "seqlens")
+    if skip_count is not None:
+        _check_counts(skip_count, 2)
+    if tile_state is not None:
+        _dev(tile_state, torch.uint8, "tile_state")
+        if tile_state.numel() != B * Hkv * (-(-M * P // 64)):
+            raise ValueError("tile_state must be [B, Hkv, ceil(max_pages * page_size / 64)]")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    with _on_device(dev, stream) as st:
+        rc = lib().sskip_attn_decode_paged(
+            _addr(q), _addr(k_pages), _addr(v_pages), _addr(block_table), _addr(seqlens), _addr(o),
+            _addr(lse), fmt, B, Hq, Hkv, N, P, M, d, sm_scale, threshold_scale_factor, num_splits,
+            _addr(workspace), ws_bytes, _addr(skip_count), _addr(tile_state), st)
+    _check(rc, "sskip_attn_decode_paged")

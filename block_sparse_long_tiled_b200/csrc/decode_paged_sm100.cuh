@@ -1,0 +1,661 @@
+// decode_paged_sm100.cuh -- split-KV Skip-Softmax decode over a paged cache,
+// in bf16 or in 4 bits.
+//
+// The rule is that of the contiguous decode: a decode tile is 64 keys and the
+// G = Hq / Hkv query heads of one kv head, the heads take one joint decision,
+// every split starts from m_run = -inf, and the splits merge by log-sum-exp.
+//
+// One CTA per (split, kv head, sequence): a producer warp follows the block
+// table and streams tiles into shared memory, four consumer warps own 16 of a
+// tile's 64 keys each.  The contractions run as m16n8k16 tensor-core products
+// with the KEYS in the 16-row dimension and the heads in the 8-column one:
+//   S^T[16 keys, 8 heads] = K Q^T,   O^T[d, 8 heads] += V^T P^T,
+// so eight heads fill the instruction (16-row query tiles would leave half of
+// it empty), and one 8x8 transpose of the packed P turns the first product's
+// result into the second's operand.  Each warp keeps O^T of its own keys in
+// registers; the warps merge once per split.  (tcgen05 has no use here: the
+// kernel is bound by HBM, and the 4-bit form wants its operands in registers,
+// where the codes are widened.)
+//
+// Without a threshold (SKIP = false) K and V tiles are fetched together, no
+// warp ever waits for another, and the softmax reference of a warp moves only
+// when a score exceeds it by 2^8.  With one, the warps exchange their tile
+// maxima (one named barrier a tile), all take the same decision, and the V
+// tile is fetched after it, kLag tiles ahead of its use; a skipped tile costs
+// no V bytes.
+#pragma once
+
+#include "kvcache_sm100.cuh"
+#include "skip_rule.cuh"
+
+namespace sskip {
+
+struct PagedDecodeParams {
+  const __nv_bfloat16* q;      // [B, Hq, D]
+  const int* seqlens;          // [B]
+  PagedRows c;
+  float* o_part;               // [B, Hq, S, D]
+  float* lse_part;             // [B, Hq, S], natural log
+  __nv_bfloat16* o;            // [B, Hq, D]
+  float* lse;                  // [B, Hq]
+  unsigned long long* counts;  // {skipped, visited} or null
+  uint8_t* tile_state;         // [B, Hkv, n_k_max] or null
+  int B, Hq, Hkv, G, S, n_k_max;
+  float scale_log2, tsf;
+};
+
+constexpr int kPgTile = 64;
+constexpr int kPgWarps = 4;                          // consumer warps
+constexpr int kPgThreads = (kPgWarps + 1) * 32;
+constexpr int kPgLag = 2;                            // P.V runs this many tiles behind the vote
+
+template <int D, bool Q4>
+struct PagedCfg {
+  static constexpr int kTileBytes = Q4 ? 4 * Kv4<D>::kRecord : kPgTile * D * 2;
+  static constexpr int kStages = Q4 ? 6 : (D == 128 ? 3 : 6);  // of K and of V
+  static constexpr int kCtas = Q4 ? 3 : 2;                      // per SM
+  static constexpr int kK = 0;
+  static constexpr int kV = kK + kStages * kTileBytes;
+  static constexpr int kMax = kV + kStages * kTileBytes;        // [2][8][W] fp32
+  static constexpr int kStat = kMax + 2 * 8 * kPgWarps * 4;     // [W][8] (m, l)
+  static constexpr int kIds = kStat + kPgWarps * 8 * 8;         // [stages][4] pages of a tile
+  static constexpr int kBar = kIds + kStages * 16;
+  static constexpr int kTotal = kBar + 4 * kStages * 8 + 16;
+  static constexpr int kAlloc = kTotal + 1024;                  // the ring starts 1024-aligned
+  static_assert(kPgWarps * 8 * (D + 4) * 4 <= kMax, "the merge of the warps fits the rings");
+  static_assert(kStages > kPgLag, "a V slot is free again when its next tile is voted on");
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The four pairs of a 4-bit word as bf16 pairs n - 8: the code under the
+// exponent of 128 is 128 + n, and taking 136 away is exact.
+__device__ __forceinline__ void widen_codes(uint32_t w, uint32_t (&r)[4]) {
+  const __nv_bfloat162 bias = __halves2bfloat162(__ushort_as_bfloat16(0x4308),
+                                                 __ushort_as_bfloat16(0x4308));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t x = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+    const __nv_bfloat162 y = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), bias);
+    r[i] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+}
+
+// n words of shared memory, n * 4 bytes aligned (n = 2 or 4).
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t (&w)[N], const uint8_t* p) {
+  if constexpr (N == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x; w[1] = v.y;
+  }
+}
+
+// (sc, mn) of a word -> the scale of n - 8 and what 0 stands for there.
+__device__ __forceinline__ void kv4_affine(uint32_t w, float& sc, float& zero) {
+  sc = __uint_as_float(w << 16);
+  zero = fmaf(8.f, sc, __uint_as_float(w & 0xFFFF0000u));
+}
+
+template <int D, bool Q4, bool SKIP>
+__global__ void __launch_bounds__(kPgThreads, PagedCfg<D, Q4>::kCtas)
+    decode_paged_kernel(const __grid_constant__ CUtensorMap map_k,
+                        const __grid_constant__ CUtensorMap map_v, const PagedDecodeParams p) {
+  using C = PagedCfg<D, Q4>;
+  constexpr int NS = C::kStages;
+  constexpr int NG = D / 32;   // 4-bit groups of a row
+  constexpr int MT = D / 16;   // 16-row tiles of O^T
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  // seqlens[b] lies in [0, max_pages * P]: another length is latched and
+  // clamped, so that no page number is read outside the sequence's table row.
+  const int cap = p.c.max_pages << p.c.page_shift;
+  const int Lraw = p.seqlens[b];
+  if ((Lraw < 0 || Lraw > cap) && tid == 0 && split == 0 && kvh == 0)
+    latch_status(kStatusInvalidArg);
+  const int Lb = min(max(Lraw, 0), cap);
+  const int n_k = (Lb + kPgTile - 1) / kPgTile;
+  const int c_per = (n_k + p.S - 1) / p.S;
+  const int j0 = split * c_per;
+  const int ntiles = max(0, min(n_k, j0 + c_per) - j0);
+  const size_t head0 = (size_t)b * p.Hq + (size_t)kvh * p.G;
+
+  if (ntiles == 0) {  // an empty split contributes nothing to the merge
+    if (p.S == 1) {
+      for (int i = tid; i < p.G * D; i += kPgThreads)
+        p.o[head0 * D + i] = __float2bfloat16_rn(0.f);
+      if (tid < p.G) p.lse[head0 + tid] = -INFINITY;
+    } else if (tid < p.G) {
+      p.lse_part[(head0 + tid) * p.S + split] = -INFINITY;
+    }
+    return;
+  }
+
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBar);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kBar + 4 * NS * 8);
+  int* ids = reinterpret_cast<int*>(smem + C::kIds);
+  const uint32_t k_smem = smem_u32(smem + C::kK), v_smem = smem_u32(smem + C::kV);
+  auto kfull = [&](int s) { return smem_u32(&bars[s]); };
+  auto kfree = [&](int s) { return smem_u32(&bars[NS + s]); };
+  auto vfull = [&](int s) { return smem_u32(&bars[2 * NS + s]); };
+  auto vfree = [&](int s) { return smem_u32(&bars[3 * NS + s]); };
+  if (tid == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(kfull(s), 1);
+      mbar_init(kfree(s), kPgWarps);
+      mbar_init(vfull(s), 1);
+      mbar_init(vfree(s), kPgWarps);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+
+  // A tile's pages: one when a page holds a tile, else 64 / P, of which those
+  // behind the last key are not fetched.
+  const int P = 1 << p.c.page_shift;
+  const int rows = min(P, kPgTile);            // of one copy
+  auto tile_copies = [&](int j) { return min(kPgTile / rows, (Lb - j * kPgTile + rows - 1) / rows); };
+  const uint32_t copy_bytes = (uint32_t)rows * (C::kTileBytes / kPgTile);
+
+  // One elected thread: the copies of tile j (of K or of V) into ring slot s.
+  auto fetch = [&](bool val, int j, int s, const int* page) {
+    const uint32_t bar = val ? vfull(s) : kfull(s);
+    const uint32_t dst = (val ? v_smem : k_smem) + s * C::kTileBytes;
+    const int n = tile_copies(j);
+    if (!dev_check(j < n_k && n >= 1 && n <= 4 && s < NS)) {
+      mbar_arrive(bar);
+      return;
+    }
+    mbar_arrive_expect_tx(bar, n * copy_bytes);
+    const int off = (j * kPgTile) & (P - 1);
+    for (int i = 0; i < n; ++i) {
+      if constexpr (Q4) {
+        const uint8_t* base = val ? p.c.v_pages : p.c.k_pages;
+        const size_t rec = (((size_t)page[i] * p.Hkv + kvh) << (p.c.page_shift - 4)) + (off >> 4);
+        bulk_load(dst + i * copy_bytes, base + rec * Kv4<D>::kRecord, copy_bytes, bar);
+      } else {
+        const int y = ((page[i] * p.Hkv + kvh) << p.c.page_shift) + off;
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h)
+          tma_load_2d(dst + h * (kPgTile * 128) + i * rows * 128, val ? &map_v : &map_k, bar,
+                      h * 64, y);
+      }
+    }
+  };
+
+  if (warp == kPgWarps) {
+    // ------------------------------------------------------------ producer
+    const int* table = p.c.block_table + (size_t)b * p.c.max_pages;
+    int issued = 0;
+    bool ok = true;
+    for (int t = 0; t < ntiles && ok; ++t) {
+      const int j = j0 + t, s = t % NS;
+      const int slot0 = (j * kPgTile) >> p.c.page_shift;
+      int page[4];
+      const int n = tile_copies(j);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        page[i] = i < n ? __ldg(table + slot0 + i) : 0;
+        if (page[i] < 0 || page[i] >= p.c.num_pages) {
+          if (lane == 0) latch_status(kStatusInvalidArg);
+          page[i] = 0;
+        }
+      }
+      if (t >= NS) {
+        ok = mbar_wait(kfree(s), ((t / NS) - 1) & 1, abort_flag);
+        if (ok && !SKIP) ok = mbar_wait(vfree(s), ((t / NS) - 1) & 1, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      if (ok && lane == 0) {
+        if (SKIP) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) ids[s * 4 + i] = page[i];
+        }
+        fetch(false, j, s, page);
+        if (!SKIP) fetch(true, j, s, page);
+        issued = t + 1;
+      }
+    }
+    __syncthreads();
+    if (*abort_flag && lane == 0) {  // wait out the copies in flight before the CTA exits
+      int no_abort = 0;
+      for (int s = 0; s < NS; ++s)
+        if (issued > s) {
+          const int last = s + (issued - 1 - s) / NS * NS;
+          mbar_wait(kfull(s), (last / NS) & 1, &no_abort);
+          if (!SKIP) mbar_wait(vfull(s), (last / NS) & 1, &no_abort);
+        }
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers
+  const int g = lane >> 2, c = lane & 3;
+  // Q^T fragments: head g, the d's that the K fragments hold at this lane.
+  uint32_t qf[MT][2];
+  float qsum[2][NG];  // sum of q over a group, heads 2 c and 2 c + 1 (4-bit)
+  {
+    const __nv_bfloat16* q = p.q + (head0 + g) * D;
+#pragma unroll
+    for (int kt = 0; kt < MT; ++kt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int d = Q4 ? (kt >> 1) * 32 + 8 * c + 2 * ((kt & 1) * 2 + i) : kt * 16 + i * 8 + 2 * c;
+        qf[kt][i] = g < p.G ? *reinterpret_cast<const uint32_t*>(q + d) : 0u;
+      }
+    if constexpr (Q4) {
+#pragma unroll
+      for (int gr = 0; gr < NG; ++gr) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w = qf[2 * gr + (i >> 1)][i & 1];
+          s += __uint_as_float(w << 16) + __uint_as_float(w & 0xFFFF0000u);
+        }
+        s += __shfl_xor_sync(0xffffffffu, s, 1);
+        s += __shfl_xor_sync(0xffffffffu, s, 2);
+        qsum[0][gr] = __shfl_sync(0xffffffffu, s, 8 * c);
+        qsum[1][gr] = __shfl_sync(0xffffffffu, s, 8 * c + 4);
+      }
+    }
+  }
+  float* wmax = reinterpret_cast<float*>(smem + C::kMax);
+  const bool t_positive = SKIP;
+  const float log2_t = SKIP ? (float)log2((double)p.tsf / (double)Lb) : -INFINITY;
+
+  float acc[MT][4];                 // O^T
+  float zacc[NG][2];                // sum of p times the groups' zeros (4-bit)
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // heads 2 c, 2 c + 1
+#pragma unroll
+  for (int i = 0; i < MT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+#pragma unroll
+  for (int i = 0; i < NG; ++i) zacc[i][0] = zacc[i][1] = 0.f;
+
+  // Scores of this warp's 16 keys of tile t, in log2 units: s[0..1] key g,
+  // s[2..3] key g + 8, heads 2 c and 2 c + 1; keys past the end -> -inf.
+  auto scores = [&](int t, float (&s)[4]) {
+    const int valid = Lb - (j0 + t) * kPgTile - warp * 16;  // of the 16
+    const uint8_t* tile = smem + C::kK + (t % NS) * C::kTileBytes;
+    if constexpr (Q4) {
+      const uint8_t* rec = tile + warp * Kv4<D>::kRecord;
+      uint32_t wa[NG], wb[NG], pa[NG], pb[NG];
+      lds_words<NG>(wa, rec + g * (D / 2) + c * NG * 4);
+      lds_words<NG>(wb, rec + (g + 8) * (D / 2) + c * NG * 4);
+      lds_words<NG>(pa, rec + Kv4<D>::kCodes + g * NG * 4);
+      lds_words<NG>(pb, rec + Kv4<D>::kCodes + (g + 8) * NG * 4);
+      s[0] = s[1] = s[2] = s[3] = 0.f;
+#pragma unroll
+      for (int gr = 0; gr < NG; ++gr) {
+        uint32_t a[4], e[4];
+        widen_codes(wa[gr], a);
+        widen_codes(wb[gr], e);
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+        mma16816(x, a[0], e[0], a[1], e[1], qf[2 * gr][0], qf[2 * gr][1]);
+        mma16816(x, a[2], e[2], a[3], e[3], qf[2 * gr + 1][0], qf[2 * gr + 1][1]);
+        float sa, za, sb, zb;
+        kv4_affine(pa[gr], sa, za);
+        kv4_affine(pb[gr], sb, zb);
+        s[0] = fmaf(sa, x[0], fmaf(za, qsum[0][gr], s[0]));
+        s[1] = fmaf(sa, x[1], fmaf(za, qsum[1][gr], s[1]));
+        s[2] = fmaf(sb, x[2], fmaf(zb, qsum[0][gr], s[2]));
+        s[3] = fmaf(sb, x[3], fmaf(zb, qsum[1][gr], s[3]));
+      }
+    } else {
+      const uint32_t base = smem_u32(tile) + warp * 16 * 128;
+      const int row = (lane & 7) + ((lane >> 3) & 1) * 8, ch = lane >> 4;
+      float x[2][4] = {};
+#pragma unroll
+      for (int kt = 0; kt < MT; ++kt) {
+        const int chunk = kt * 2 + ch;
+        uint32_t a[4];
+        ldsm4(base + (chunk >> 3) * (kPgTile * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4), a);
+        mma16816(x[kt & 1], a[0], a[1], a[2], a[3], qf[kt][0], qf[kt][1]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] = x[0][i] + x[1][i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      s[i] = (g + (i >> 1) * 8 < valid) ? s[i] * p.scale_log2 : -INFINITY;
+  };
+
+  // O^T = a O^T + V^T P^T over this warp's 16 keys of tile t, from ring slot t % NS.
+  auto accumulate = [&](int t, const float (&pr)[4], float a0, float a1) {
+    const int valid = Lb - (j0 + t) * kPgTile - warp * 16;
+    uint8_t* tile = smem + C::kV + (t % NS) * C::kTileBytes;
+    if (__any_sync(0xffffffffu, a0 != 1.f || a1 != 1.f)) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        acc[i][0] *= a0; acc[i][1] *= a1; acc[i][2] *= a0; acc[i][3] *= a1;
+      }
+#pragma unroll
+      for (int i = 0; i < NG; ++i) { zacc[i][0] *= a0; zacc[i][1] *= a1; }
+    }
+    if (valid <= 0) return;
+    if constexpr (Q4) {
+      const uint8_t* rec = tile + warp * Kv4<D>::kRecord;
+      uint32_t w0[NG], w1[NG], pa[NG], pb[NG];
+      lds_words<NG>(w0, rec + lane * NG * 4);
+      lds_words<NG>(w1, rec + (32 + lane) * NG * 4);
+      lds_words<NG>(pa, rec + Kv4<D>::kCodes + g * NG * 4);
+      lds_words<NG>(pb, rec + Kv4<D>::kCodes + (g + 8) * NG * 4);
+#pragma unroll
+      for (int gr = 0; gr < NG; ++gr) {
+        float sa, za, sb, zb;
+        kv4_affine(pa[gr], sa, za);
+        kv4_affine(pb[gr], sb, zb);
+        // Behind the last key the record holds what an earlier sequence left:
+        // its codes are numbers, its scales need not be.
+        if (g >= valid) sa = za = 0.f;
+        if (g + 8 >= valid) sb = zb = 0.f;
+        zacc[gr][0] = fmaf(pr[0], za, fmaf(pr[2], zb, zacc[gr][0]));
+        zacc[gr][1] = fmaf(pr[1], za, fmaf(pr[3], zb, zacc[gr][1]));
+        // The scale joins P before its rounding to bf16 (2^-9 of the product).
+        const uint32_t b0 = transpose8x8(pack_bf16x2(pr[0] * sa, pr[1] * sa));
+        const uint32_t b1 = transpose8x8(pack_bf16x2(pr[2] * sb, pr[3] * sb));
+        uint32_t a[4], e[4];
+        widen_codes(w0[gr], a);
+        widen_codes(w1[gr], e);
+        mma16816(acc[2 * gr], a[0], a[1], e[0], e[1], b0, b1);
+        mma16816(acc[2 * gr + 1], a[2], a[3], e[2], e[3], b0, b1);
+      }
+    } else {
+      if (valid < 16) {  // rows behind the last key: P is 0 there, V may be NaN
+        for (int i = lane; i < (16 - valid) * 8; i += 32)
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            *reinterpret_cast<uint4*>(tile + h * (kPgTile * 128) +
+                                      (warp * 16 + valid + (i >> 3)) * 128 + (i & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+        __syncwarp();
+      }
+      // P is rounded to bf16 for the product (2^-9 of each weight); l is not.
+      const uint32_t b0 = transpose8x8(pack_bf16x2(pr[0], pr[1]));
+      const uint32_t b1 = transpose8x8(pack_bf16x2(pr[2], pr[3]));
+      const uint32_t base = smem_u32(tile) + warp * 16 * 128;
+      const int row = (lane & 7) + (lane >> 4) * 8, ch = (lane >> 3) & 1;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const int chunk = mt * 2 + ch;
+        uint32_t a[4];
+        ldsm4_t(base + (chunk >> 3) * (kPgTile * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4),
+                a);
+        mma16816(acc[mt], a[0], a[1], a[2], a[3], b0, b1);
+      }
+    }
+  };
+
+  int n_skipped = 0;
+  uint32_t v_used = 0, v_par = 0;  // warp 0 lane 0: V slots in use, parity of their last copy
+  if constexpr (!SKIP) {
+    for (int t = 0; t < ntiles; ++t) {
+      const int s = t % NS;
+      mbar_wait(kfull(s), (t / NS) & 1, abort_flag);
+      float x[4];
+      scores(t, x);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(kfree(s));
+      // The reference moves only when a score is 2^8 above it: P stays below
+      // 2^8 and most tiles need no exchange between the lanes.
+      float a[2] = {1.f, 1.f};
+      float top[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
+      if (__any_sync(0xffffffffu, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f)) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1)
+            top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+          const float mn = fmaxf(m[i], top[i]);
+          a[i] = (m[i] == -INFINITY) ? 0.f : ex2_approx(m[i] - mn);
+          m[i] = mn;
+          l[i] *= a[i];
+        }
+      }
+      float pr[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float ref = m[i & 1] == -INFINITY ? 0.f : m[i & 1];
+        pr[i] = ex2_approx(x[i] - ref);
+        l[i & 1] += pr[i];
+      }
+      if (p.tile_state && tid == 0)
+        p.tile_state[((size_t)b * p.Hkv + kvh) * p.n_k_max + j0 + t] = 1;
+      mbar_wait(vfull(s), (t / NS) & 1, abort_flag);
+      accumulate(t, pr, a[0], a[1]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(vfree(s));
+    }
+  } else {
+    float pr[kPgLag][4], al[kPgLag][2];
+    uint32_t kept = 0, v_phase = 0;  // kept: bit 0 the last tile, bit 1 the one before
+#pragma unroll
+    for (int i = 0; i < kPgLag; ++i) {
+      pr[i][0] = pr[i][1] = pr[i][2] = pr[i][3] = 0.f;
+      al[i][0] = al[i][1] = 1.f;
+    }
+    for (int t = 0; t < ntiles + kPgLag; ++t) {
+      const bool live = t < ntiles;
+      float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      int page[4];
+      if (live) {
+        const int s = t % NS;
+        mbar_wait(kfull(s), (t / NS) & 1, abort_flag);
+        if (tid == 0) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) page[i] = ids[s * 4 + i];
+        }
+        scores(t, x);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(kfree(s));
+        float top[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1)
+            top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+          if (g == 0) wmax[((t & 1) * 8 + 2 * c + i) * kPgWarps + warp] = top[i];
+        }
+      }
+      named_bar_sync(1, kPgWarps * 32);  // maxima of tile t published; P.V of t - 1 - kLag done
+      float np[4] = {0.f, 0.f, 0.f, 0.f}, na[2] = {1.f, 1.f};
+      bool keep = false;
+      if (live) {
+        float top[2];
+        bool pass = true;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float4 w = *reinterpret_cast<const float4*>(&wmax[((t & 1) * 8 + 2 * c + i) * kPgWarps]);
+          top[i] = fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w));
+          if (2 * c + i < p.G) pass = pass && row_passes_log2(top[i], m[i], log2_t, t_positive);
+        }
+        keep = !__all_sync(0xffffffffu, pass);
+        if (keep) {
+          if (tid == 0 && !*abort_flag) {
+            fetch(true, j0 + t, t % NS, page);
+            v_used |= 1u << (t % NS);
+            v_par ^= 1u << (t % NS);
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float mn = fmaxf(m[i], top[i]);
+            na[i] = (m[i] == -INFINITY) ? 0.f : ex2_approx(m[i] - mn);
+            m[i] = mn;
+            l[i] *= na[i];
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            np[i] = ex2_approx(x[i] - (m[i & 1] == -INFINITY ? 0.f : m[i & 1]));
+            l[i & 1] += np[i];
+          }
+        } else {
+          n_skipped += 1;
+        }
+        if (p.tile_state && tid == 0)
+          p.tile_state[((size_t)b * p.Hkv + kvh) * p.n_k_max + j0 + t] = keep ? 1 : 2;
+      }
+      const int u = t - kPgLag;
+      if (u >= 0 && ((kept >> (kPgLag - 1)) & 1)) {
+        const int s = u % NS;
+        mbar_wait(vfull(s), (v_phase >> s) & 1, abort_flag);
+        v_phase ^= 1u << s;
+        accumulate(u, pr[kPgLag - 1], al[kPgLag - 1][0], al[kPgLag - 1][1]);
+      }
+      kept = (kept << 1) | (keep ? 1u : 0u);
+#pragma unroll
+      for (int i = kPgLag - 1; i >= 0; --i) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) pr[i][k] = i ? pr[i - 1][k] : np[k];
+        al[i][0] = i ? al[i - 1][0] : na[0];
+        al[i][1] = i ? al[i - 1][1] : na[1];
+      }
+    }
+  }
+
+  // ---- merge the warps' O^T, row sums and references; write the split.
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
+      if constexpr (Q4) {
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr)
+          zacc[gr][i] += __shfl_xor_sync(0xffffffffu, zacc[gr][i], o);
+      }
+    }
+  __syncthreads();  // with the producer: every warp is past its last use of the rings
+  if (*abort_flag) {
+    if (SKIP && tid == 0) {
+      int no_abort = 0;
+      for (int s = 0; s < NS; ++s)
+        if ((v_used >> s) & 1) mbar_wait(vfull(s), ((v_par >> s) & 1) ^ 1, &no_abort);
+    }
+    return;
+  }
+  constexpr int RS = D + 4;  // row stride of the merge buffer: spreads the banks
+  float* red = reinterpret_cast<float*>(smem);
+  float2* stat = reinterpret_cast<float2*>(smem + C::kStat);
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int d = Q4 ? (mt >> 1) * 32 + 4 * g + 2 * (mt & 1) + (i >> 1) : mt * 16 + g + (i >> 1) * 8;
+      const int h = 2 * c + (i & 1);
+      red[(warp * 8 + h) * RS + d] = acc[mt][i] + (Q4 ? zacc[mt >> 1][i & 1] : 0.f);
+    }
+  if (g == 0) {
+    stat[warp * 8 + 2 * c] = make_float2(m[0], l[0]);
+    stat[warp * 8 + 2 * c + 1] = make_float2(m[1], l[1]);
+  }
+  named_bar_sync(1, kPgWarps * 32);
+  if (tid == 0 && p.counts) {
+    atomicAdd(&p.counts[0], (unsigned long long)n_skipped);
+    atomicAdd(&p.counts[1], (unsigned long long)ntiles);
+  }
+  for (int i = tid; i < p.G * D; i += kPgWarps * 32) {
+    const int h = i / D, d = i % D;
+    float2 st[kPgWarps];
+    float mx = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kPgWarps; ++w) {
+      st[w] = stat[w * 8 + h];
+      mx = fmaxf(mx, st[w].x);
+    }
+    float sum = 0.f, o = 0.f;
+#pragma unroll
+    for (int w = 0; w < kPgWarps; ++w) {
+      const float e = st[w].x == -INFINITY ? 0.f : ex2_approx(st[w].x - mx);
+      sum = fmaf(e, st[w].y, sum);
+      o = fmaf(e, red[(w * 8 + h) * RS + d], o);
+    }
+    const float lse = (mx + __log2f(sum)) * 0.69314718055994531f;
+    if (p.S == 1) {
+      p.o[(head0 + h) * D + d] = __float2bfloat16_rn(o / sum);
+      if (d == 0) p.lse[head0 + h] = lse;
+    } else {
+      p.o_part[((head0 + h) * p.S + split) * D + d] = o / sum;
+      if (d == 0) p.lse_part[(head0 + h) * p.S + split] = lse;
+    }
+  }
+}
+
+// Merge the splits of one (sequence, query head).
+template <int D>
+__global__ void __launch_bounds__(128) decode_paged_combine_kernel(const PagedDecodeParams p) {
+  const size_t bh = blockIdx.x;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const float* lp = p.lse_part + bh * p.S;
+  __shared__ float w_s[64];
+  __shared__ float red[4][D];
+  __shared__ float sum_s;
+  if (warp == 0) {
+    const float a = lane < p.S ? lp[lane] : -INFINITY;
+    const float e = lane + 32 < p.S ? lp[lane + 32] : -INFINITY;
+    float mx = fmaxf(a, e);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float wa = a == -INFINITY ? 0.f : __expf(a - mx);
+    const float we = e == -INFINITY ? 0.f : __expf(e - mx);
+    float sum = wa + we;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    w_s[lane] = wa;
+    w_s[lane + 32] = we;
+    if (lane == 0) {
+      sum_s = sum;
+      // Every split empty (a sequence of length 0): O = 0 and lse = -inf.
+      p.lse[bh] = mx == -INFINITY ? -INFINITY : mx + __logf(sum);
+    }
+  }
+  __syncthreads();
+  constexpr int V = D / 32;  // columns of a lane
+  float o[V] = {};
+  for (int s = warp; s < p.S; s += 4) {
+    const float w = w_s[s];
+    if (w == 0.f) continue;  // an empty split wrote no partial
+    const float* part = p.o_part + (bh * p.S + s) * D + lane * V;
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = fmaf(w, part[i], o[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) red[warp][lane * V + i] = o[i];
+  __syncthreads();
+  for (int d = tid; d < D; d += 128) {
+    const float x = red[0][d] + red[1][d] + red[2][d] + red[3][d];
+    const float sum = sum_s;
+    p.o[bh * D + d] = __float2bfloat16_rn(sum == 0.f ? 0.f : x / sum);
+  }
+}
+
+}  // namespace sskip

@@ -71,15 +71,6 @@ struct DecodeSmem {
   static_assert(kDecWarps * G * D * 4 <= kDecNK * kTileBytes, "reduction scratch fits the K ring");
 };
 
-__device__ __forceinline__ void bf16x8_to_f32(const uint4& w, float (&f)[8]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(u[i] << 16);
-    f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-  }
-}
-
 // Reduce G partial dot products over the 8 lanes of a key group so that lane
 // `sub` ends with the full sum for head sub / (8 / G): at each halving step a
 // lane keeps the half of the heads selected by its lane bit and receives the

@@ -1,0 +1,136 @@
+// kv4_sm100.cuh -- the 4-bit form of keys and values in the paged cache.
+//
+// 32 neighbouring values of a row share a scale and a minimum, both bf16:
+//   mn = min rounded down, sc = (max - mn) / 15 rounded up, n = rint((x - mn) / sc)
+// clamped to 0 .. 15, and the value read back is sc n + mn.  Rounding mn down
+// and sc up keeps every value inside [mn, mn + 15 sc], so no value is off by
+// more than sc / 2.  The quotients are true divisions: with the bf16 inputs of
+// the values exact ties are common, and they must go to the even code whatever
+// the device.  A group that holds a NaN or an infinity, or whose spread does
+// not fit, reads back as NaN.
+//
+// A record is 16 rows of one head: the codes (8 D bytes), then [16][D / 32]
+// pairs (sc, mn).  The code order is the one in which a warp's m16n8k16
+// tensor-core fragments are made from it without an exchange, each lane from
+// whole 16-byte (D = 64: 8-byte) pieces:
+//   keys:   row r at r D / 2; a 32-bit word holds the 8 values d = 8 m .. 8 m + 7,
+//           value 2 i in nibble i and 2 i + 1 in nibble i + 4, so a mask and a
+//           shift leave neighbouring values in the two halves of a register;
+//           word m stands at (m % 4) (D / 32) + m / 4: a lane's words, one of
+//           each group, are contiguous.
+//   values: a 32-bit word holds the same 4 values d = 32 g' + 4 g + i of two
+//           neighbouring rows r, r + 1 (low and high half, nibble i); the words
+//           of the D / 32 groups g' are contiguous, at lane 4 g + (r / 2) % 4,
+//           the two halves of the record (r / 8) after each other.
+#pragma once
+
+#include <cfloat>
+#include <cstdint>
+
+#include "sm100_ptx.cuh"
+
+namespace sskip {
+
+template <int D>
+struct Kv4 {
+  static constexpr int kGroups = D / 32;
+  static constexpr int kCodes = 8 * D;              // bytes of 16 rows' codes
+  static constexpr int kRecord = kCodes + 16 * kGroups * 4;
+};
+
+__device__ __forceinline__ void kv4_bounds(const float (&x)[8], float& lo, float& hi) {
+  lo = INFINITY;
+  hi = -INFINITY;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const bool finite = fabsf(x[e]) <= FLT_MAX;
+    lo = fminf(lo, finite ? x[e] : -INFINITY);
+    hi = fmaxf(hi, finite ? x[e] : INFINITY);
+  }
+}
+
+// Store row r of a record.  The D / 16 lanes of a head hold chunks m0 and m1
+// (8 values each) of it; all 32 lanes call, `live` ones write.
+template <int D>
+__device__ __forceinline__ void kv4_store_row(uint8_t* rec, int r, bool value, bool live, int m0,
+                                              int m1, const float (&x0)[8], const float (&x1)[8]) {
+  constexpr int LH = D / 16, NG = Kv4<D>::kGroups;
+  float lo0, hi0, lo1, hi1, glo[2], ghi[2];
+  kv4_bounds(x0, lo0, hi0);
+  kv4_bounds(x1, lo1, hi1);
+  glo[0] = glo[1] = ghi[0] = ghi[1] = 0.f;
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    float lo = fminf((m0 >> 2) == g ? lo0 : INFINITY, (m1 >> 2) == g ? lo1 : INFINITY);
+    float hi = fmaxf((m0 >> 2) == g ? hi0 : -INFINITY, (m1 >> 2) == g ? hi1 : -INFINITY);
+#pragma unroll
+    for (int o = LH / 2; o > 0; o >>= 1) {
+      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+    if ((m0 >> 2) == g) { glo[0] = lo; ghi[0] = hi; }
+    if ((m1 >> 2) == g) { glo[1] = lo; ghi[1] = hi; }
+  }
+  if (!live) return;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int m = i ? m1 : m0;
+    const __nv_bfloat16 mnb = __float2bfloat16_rd(glo[i]);
+    float mn = __bfloat162float(mnb);
+    float sc = __bfloat162float(__float2bfloat16_ru(__fdiv_rn(ghi[i] - mn, 15.f)));
+    const bool bad = !(sc <= FLT_MAX) || !(fabsf(mn) <= FLT_MAX);
+    uint32_t n[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float x = i ? x1[e] : x0[e];
+      const float y = rintf(__fdiv_rn(x - mn, sc));
+      n[e] = (sc > 0.f && !bad) ? (uint32_t)fminf(fmaxf(y, 0.f), 15.f) : 0u;
+    }
+    if ((m & 3) == 0) {
+      uint32_t w = bad ? 0x7FFF7FFFu : pack_bf16x2(sc, mn);
+      *reinterpret_cast<uint32_t*>(rec + Kv4<D>::kCodes + (r * NG + (m >> 2)) * 4) = w;
+    }
+    if (!value) {
+      uint32_t w = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w |= n[e] << (4 * ((e >> 1) + (e & 1) * 4));
+      *reinterpret_cast<uint32_t*>(rec + r * (D / 2) + ((m & 3) * NG + (m >> 2)) * 4) = w;
+    } else {
+#pragma unroll
+      for (int qd = 0; qd < 2; ++qd) {
+        const int g = (2 * m + qd) & 7;
+        const uint32_t w = n[4 * qd] | n[4 * qd + 1] << 4 | n[4 * qd + 2] << 8 | n[4 * qd + 3] << 12;
+        *reinterpret_cast<uint16_t*>(rec + ((r >> 3) * 32 + g * 4 + ((r >> 1) & 3)) * NG * 4 +
+                                     (m >> 2) * 4 + (r & 1) * 2) = (uint16_t)w;
+      }
+    }
+  }
+}
+
+// Values 8 m .. 8 m + 7 of row r.
+template <int D>
+__device__ __forceinline__ void kv4_load_chunk(const uint8_t* rec, int r, bool value, int m,
+                                               float (&x)[8]) {
+  constexpr int NG = Kv4<D>::kGroups;
+  const uint32_t par = *reinterpret_cast<const uint32_t*>(rec + Kv4<D>::kCodes +
+                                                          (r * NG + (m >> 2)) * 4);
+  const float sc = __uint_as_float(par << 16), mn = __uint_as_float(par & 0xFFFF0000u);
+  if (!value) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(rec + r * (D / 2) +
+                                                          ((m & 3) * NG + (m >> 2)) * 4);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      x[e] = fmaf((float)((w >> (4 * ((e >> 1) + (e & 1) * 4))) & 15u), sc, mn);
+  } else {
+#pragma unroll
+    for (int qd = 0; qd < 2; ++qd) {
+      const int g = (2 * m + qd) & 7;
+      const uint32_t w = *reinterpret_cast<const uint16_t*>(
+          rec + ((r >> 3) * 32 + g * 4 + ((r >> 1) & 3)) * NG * 4 + (m >> 2) * 4 + (r & 1) * 2);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[4 * qd + i] = fmaf((float)((w >> (4 * i)) & 15u), sc, mn);
+    }
+  }
+}
+
+}  // namespace sskip

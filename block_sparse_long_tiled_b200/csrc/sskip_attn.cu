@@ -16,7 +16,9 @@
 #include <vector>
 
 #include "../../include/sskip_attn.h"
+#include "decode_paged_sm100.cuh"
 #include "decode_sm100.cuh"
+#include "kvcache_sm100.cuh"
 #include "permute_sm100.cuh"
 #include "prefill_sm100.cuh"
 
@@ -762,4 +764,340 @@ SSKIP_API int sskip_attn_decode_host(const void* q_h, const int* seqlens_h, void
       cudaMemcpyAsync(lse_h, lse_d, ln, cudaMemcpyDeviceToHost, st) != cudaSuccess)
     return SSKIP_ERR_CUDA;
   return SSKIP_OK;
+}
+
+// ---------------------------------------------------------------------------
+// The paged key/value cache: rotation + append, read-back, and the decode.
+namespace sskip {
+namespace {
+
+bool misaligned(const void* p, uintptr_t mask) {
+  return (reinterpret_cast<uintptr_t>(p) & mask) != 0;
+}
+
+// The host checks every call over a paged cache makes.
+int paged_check(const void* k_pages, const void* v_pages, const int* block_table, int kv_format,
+                int num_pages, int page_size, int max_pages, int B, int Hkv, int d) {
+  if (!k_pages || !v_pages || k_pages == v_pages || !block_table) return SSKIP_ERR_INVALID_ARG;
+  if (!aligned16(k_pages) || !aligned16(v_pages) || misaligned(block_table, 3))
+    return SSKIP_ERR_INVALID_ARG;
+  if (B < 1 || Hkv < 1 || num_pages < 1 || max_pages < 1 || page_size < 1)
+    return SSKIP_ERR_INVALID_ARG;
+  if (kv_format != SSKIP_KV_BF16 && kv_format != SSKIP_KV_INT4) return SSKIP_ERR_UNSUPPORTED;
+  if (d != 64 && d != 128) return SSKIP_ERR_UNSUPPORTED;
+  if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)))
+    return SSKIP_ERR_UNSUPPORTED;
+  // Positions of a sequence and rows of the cache are 32-bit coordinates.
+  if ((long long)max_pages * page_size > 0x7FFFFFFFll ||
+      (long long)num_pages * Hkv > 0x7FFFFFFFll / page_size)
+    return SSKIP_ERR_UNSUPPORTED;
+  return SSKIP_OK;
+}
+
+PagedRows paged_rows(void* k_pages, void* v_pages, const int* block_table, int num_pages,
+                     int page_size, int max_pages, int B, int Hkv) {
+  PagedRows c{};
+  c.k_pages = static_cast<uint8_t*>(k_pages);
+  c.v_pages = static_cast<uint8_t*>(v_pages);
+  c.block_table = block_table;
+  c.B = B; c.Hkv = Hkv; c.num_pages = num_pages; c.max_pages = max_pages;
+  while ((1 << c.page_shift) < page_size) ++c.page_shift;
+  return c;
+}
+
+// A token's heads go to as many warps as it takes to fill the GPU.
+int kv_warps_per_token(int T, int units, int heads_per_warp) {
+  const int most = (units + heads_per_warp - 1) / heads_per_warp;
+  return (int)std::min<long long>(most, std::max<long long>(1, 148ll * 64 / T));
+}
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + nb && y < x + na;
+}
+
+// 2-D bf16 map over the rows of every page and head, box {64, box_rows},
+// 128-byte swizzle.
+bool make_page_map(CUtensorMap* map, const void* base, int d, long long rows, int box_rows) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)d * 2};
+  cuuint32_t box[2] = {64u, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1u, 1u};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool Q4, bool SKIP>
+int launch_decode_paged(const CUtensorMap& mk, const CUtensorMap& mv, const PagedDecodeParams& p,
+                        cudaStream_t st) {
+  auto kernel = decode_paged_kernel<D, Q4, SKIP>;
+  const int smem = PagedCfg<D, Q4>::kAlloc;
+  if (ensure_smem(reinterpret_cast<const void*>(kernel), smem) != cudaSuccess)
+    return SSKIP_ERR_CUDA;
+  kernel<<<dim3(p.S, p.Hkv, p.B), kPgThreads, smem, st>>>(mk, mv, p);
+  if (cudaGetLastError() != cudaSuccess) return SSKIP_ERR_CUDA;
+  if (p.S == 1) return SSKIP_OK;
+  decode_paged_combine_kernel<D><<<(unsigned)(p.B * p.Hq), 128, 0, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? SSKIP_OK : SSKIP_ERR_CUDA;
+}
+
+template <int D, bool Q4>
+int launch_decode_paged(const CUtensorMap& mk, const CUtensorMap& mv, const PagedDecodeParams& p,
+                        cudaStream_t st) {
+  return p.tsf > 0.f ? launch_decode_paged<D, Q4, true>(mk, mv, p, st)
+                     : launch_decode_paged<D, Q4, false>(mk, mv, p, st);
+}
+
+}  // namespace
+}  // namespace sskip
+
+SSKIP_API size_t sskip_kv_page_bytes(int kv_format, int Hkv, int page_size, int d) {
+  if (Hkv < 1 || page_size < 16 || page_size > 256 || (page_size & (page_size - 1)) ||
+      (d != 64 && d != 128))
+    return 0;
+  const size_t rows = (size_t)Hkv * page_size;
+  if (kv_format == SSKIP_KV_BF16) return rows * d * 2;
+  if (kv_format == SSKIP_KV_INT4)
+    return rows / 16 * (d == 128 ? Kv4<128>::kRecord : Kv4<64>::kRecord);
+  return 0;
+}
+
+SSKIP_API int sskip_rope_freqs(int rot_dim, double base, int scaling, double factor,
+                               double slow_turns, double fast_turns, double original_len,
+                               uint64_t* turns, double* attn_factor) {
+  if (!turns || rot_dim < 2 || rot_dim % 2 != 0 || !(base > 1.0) || !std::isfinite(base))
+    return SSKIP_ERR_INVALID_ARG;
+  if (scaling < SSKIP_ROPE_PLAIN || scaling > SSKIP_ROPE_YARN) return SSKIP_ERR_UNSUPPORTED;
+  if (scaling != SSKIP_ROPE_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor)))
+    return SSKIP_ERR_INVALID_ARG;
+  if ((scaling == SSKIP_ROPE_BANDS || scaling == SSKIP_ROPE_YARN) &&
+      (!(slow_turns > 0.0) || !(fast_turns > slow_turns) || !std::isfinite(fast_turns) ||
+       !(original_len >= 1.0) || !std::isfinite(original_len)))
+    return SSKIP_ERR_INVALID_ARG;
+  const double two_pi = 6.283185307179586476925;
+  // The pair (as a real number) that makes n turns over the original context.
+  auto pair_of = [&](double n) {
+    return rot_dim * std::log(original_len / (n * two_pi)) / (2.0 * std::log(base));
+  };
+  double lo = 0.0, hi = 0.0;
+  if (scaling == SSKIP_ROPE_YARN) {
+    lo = std::max(std::floor(pair_of(fast_turns)), 0.0);
+    hi = std::min(std::ceil(pair_of(slow_turns)), (double)rot_dim - 1.0);
+  }
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / rot_dim);
+    if (scaling == SSKIP_ROPE_LINEAR) {
+      f /= factor;
+    } else if (scaling == SSKIP_ROPE_BANDS) {
+      const double n = original_len * f / two_pi;  // turns over the original context
+      const double keep =
+          std::min(1.0, std::max(0.0, (n - slow_turns) / (fast_turns - slow_turns)));
+      f = f * (keep + (1.0 - keep) / factor);
+    } else if (scaling == SSKIP_ROPE_YARN) {
+      const double ramp = std::min(1.0, std::max(0.0, (i - lo) / std::max(hi - lo, 0.001)));
+      f = f * (1.0 - ramp) + f / factor * ramp;
+    }
+    turns[i] = (uint64_t)std::nearbyint(std::ldexp(f / two_pi, 64));
+  }
+  if (attn_factor)
+    *attn_factor = scaling == SSKIP_ROPE_YARN ? 0.1 * std::log(factor) + 1.0 : 1.0;
+  return SSKIP_OK;
+}
+
+SSKIP_API int sskip_kv_append(const void* q, const void* k, const void* v, long long q_stride,
+                              long long k_stride, long long v_stride, const int* seq_ids,
+                              const int* positions, const void* q_weight, const void* k_weight,
+                              float eps, const uint64_t* turns, int rot_dim, int interleaved,
+                              float attn_factor, void* q_out, void* k_out, void* v_out,
+                              int out_len, void* k_pages, void* v_pages, const int* block_table,
+                              int kv_format, int num_pages, int page_size, int max_pages, int T,
+                              int B, int Hq, int Hkv, int d, void* stream) {
+  if (T < 0 || Hq < 0 || Hkv < 0 || Hq + Hkv < 1 || out_len < 1) return SSKIP_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return SSKIP_ERR_UNSUPPORTED;
+  if (rot_dim < 0 || rot_dim > d || !std::isfinite(attn_factor)) return SSKIP_ERR_INVALID_ARG;
+  if (rot_dim % 16 != 0) return SSKIP_ERR_UNSUPPORTED;
+  if (T == 0) return SSKIP_OK;
+  if (T % out_len != 0) return SSKIP_ERR_INVALID_ARG;
+  const bool cached = k_pages || v_pages;
+  if (Hq > 0 ? (!q || !q_out) : (q || q_out || q_weight)) return SSKIP_ERR_INVALID_ARG;
+  if (Hkv > 0 ? (!k || !v || (!cached && !k_out)) : (k || v || cached || k_out || k_weight))
+    return SSKIP_ERR_INVALID_ARG;
+  if (!k_out != !v_out) return SSKIP_ERR_INVALID_ARG;
+  if ((q_weight || k_weight) && (!(eps >= 0.f) || !std::isfinite(eps)))
+    return SSKIP_ERR_INVALID_ARG;
+  if ((rot_dim > 0 && (!turns || !positions)) || (cached && (!seq_ids || !positions)))
+    return SSKIP_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_out) ||
+      !aligned16(v_out) || !aligned16(q_weight) || !aligned16(k_weight) || misaligned(turns, 7) ||
+      misaligned(seq_ids, 3) || misaligned(positions, 3))
+    return SSKIP_ERR_INVALID_ARG;
+  if ((Hq && (q_stride < (long long)Hq * d || q_stride % 8)) ||
+      (Hkv && (k_stride < (long long)Hkv * d || k_stride % 8 ||
+               v_stride < (long long)Hkv * d || v_stride % 8)))
+    return SSKIP_ERR_INVALID_ARG;
+  if (cached) {
+    const int rc = paged_check(k_pages, v_pages, block_table, kv_format, num_pages, page_size,
+                               max_pages, B, Hkv, d);
+    if (rc != SSKIP_OK) return rc;
+  }
+  const int units = Hq + 2 * Hkv, heads = 32 / (d / 16);
+  const int wpt = kv_warps_per_token(T, units, heads);
+  const long long warps = (long long)T * wpt;
+  if (warps > 0x7FFFFFFFll - 8 || units > (1 << 20)) return SSKIP_ERR_UNSUPPORTED;
+  // Rows are written while others are still read: no output may share memory
+  // with an input or another output.
+  {
+    struct Range { const void* p; size_t n; bool out; };
+    const size_t qn = (size_t)T * Hq * d * 2, kn = (size_t)T * Hkv * d * 2;
+    auto span = [&](long long stride, int H) { return ((size_t)(T - 1) * stride + (size_t)H * d) * 2; };
+    const size_t pages = cached ? num_pages * sskip_kv_page_bytes(kv_format, Hkv, page_size, d) : 0;
+    const Range r[] = {{q, Hq ? span(q_stride, Hq) : 0, false}, {k, Hkv ? span(k_stride, Hkv) : 0, false},
+                       {v, Hkv ? span(v_stride, Hkv) : 0, false}, {q_out, qn, true},
+                       {k_out, kn, true}, {v_out, kn, true}, {k_pages, pages, true},
+                       {v_pages, pages, true}};
+    for (int i = 0; i < 8; ++i)
+      for (int j = i + 1; j < 8; ++j)
+        if ((r[i].out || r[j].out) && overlap(r[i].p, r[i].n, r[j].p, r[j].n))
+          return SSKIP_ERR_INVALID_ARG;
+  }
+  AppendParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.q_stride = q_stride; p.k_stride = k_stride; p.v_stride = v_stride;
+  p.seq_ids = seq_ids;
+  p.positions = positions;
+  p.q_weight = static_cast<const __nv_bfloat16*>(q_weight);
+  p.k_weight = static_cast<const __nv_bfloat16*>(k_weight);
+  p.eps = eps;
+  p.turns = reinterpret_cast<const unsigned long long*>(turns);
+  p.rot_chunks = rot_dim / 16;
+  p.interleaved = interleaved != 0;
+  p.attn_factor = attn_factor;
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.k_out = static_cast<__nv_bfloat16*>(k_out);
+  p.v_out = static_cast<__nv_bfloat16*>(v_out);
+  p.out_len = out_len; p.T = T; p.Hq = Hq; p.warps_per_token = wpt;
+  if (cached)
+    p.c = paged_rows(k_pages, v_pages, block_table, num_pages, page_size, max_pages, B, Hkv);
+  p.c.Hkv = Hkv;
+  const unsigned grid = (unsigned)((warps + kKvThreads / 32 - 1) / (kKvThreads / 32));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool q4 = cached && kv_format == SSKIP_KV_INT4;
+  if (d == 128) {
+    if (q4) kv_append_kernel<128, true><<<grid, kKvThreads, 0, st>>>(p);
+    else kv_append_kernel<128, false><<<grid, kKvThreads, 0, st>>>(p);
+  } else {
+    if (q4) kv_append_kernel<64, true><<<grid, kKvThreads, 0, st>>>(p);
+    else kv_append_kernel<64, false><<<grid, kKvThreads, 0, st>>>(p);
+  }
+  return cudaGetLastError() == cudaSuccess ? SSKIP_OK : SSKIP_ERR_CUDA;
+}
+
+SSKIP_API int sskip_kv_gather(const void* k_pages, const void* v_pages, const int* block_table,
+                              const int* seq_ids, const int* positions, void* k_out, void* v_out,
+                              int out_len, int kv_format, int num_pages, int page_size,
+                              int max_pages, int T, int B, int Hkv, int d, void* stream) {
+  if (T < 0 || out_len < 1) return SSKIP_ERR_INVALID_ARG;
+  int rc = paged_check(k_pages, v_pages, block_table, kv_format, num_pages, page_size, max_pages,
+                       B, Hkv, d);
+  if (rc != SSKIP_OK || T == 0) return rc;
+  if (T % out_len != 0 || !seq_ids || !positions || !k_out || !v_out || !aligned16(k_out) ||
+      !aligned16(v_out) || misaligned(seq_ids, 3) || misaligned(positions, 3))
+    return SSKIP_ERR_INVALID_ARG;
+  const int wpt = kv_warps_per_token(T, 2 * Hkv, 32 / (d / 16));
+  const long long warps = (long long)T * wpt;
+  if (warps > 0x7FFFFFFFll - 8 || Hkv > (1 << 19)) return SSKIP_ERR_UNSUPPORTED;
+  const size_t on = (size_t)T * Hkv * d * 2;
+  const size_t pages = num_pages * sskip_kv_page_bytes(kv_format, Hkv, page_size, d);
+  if (overlap(k_out, on, v_out, on) || overlap(k_out, on, k_pages, pages) ||
+      overlap(k_out, on, v_pages, pages) || overlap(v_out, on, k_pages, pages) ||
+      overlap(v_out, on, v_pages, pages))
+    return SSKIP_ERR_INVALID_ARG;
+  GatherParams p{};
+  p.seq_ids = seq_ids;
+  p.positions = positions;
+  p.k_out = static_cast<__nv_bfloat16*>(k_out);
+  p.v_out = static_cast<__nv_bfloat16*>(v_out);
+  p.out_len = out_len; p.T = T; p.warps_per_token = wpt;
+  p.c = paged_rows(const_cast<void*>(k_pages), const_cast<void*>(v_pages), block_table, num_pages,
+                   page_size, max_pages, B, Hkv);
+  const unsigned grid = (unsigned)((warps + kKvThreads / 32 - 1) / (kKvThreads / 32));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (kv_format == SSKIP_KV_INT4) {
+    if (d == 128) kv_gather_kernel<128, true><<<grid, kKvThreads, 0, st>>>(p);
+    else kv_gather_kernel<64, true><<<grid, kKvThreads, 0, st>>>(p);
+  } else {
+    if (d == 128) kv_gather_kernel<128, false><<<grid, kKvThreads, 0, st>>>(p);
+    else kv_gather_kernel<64, false><<<grid, kKvThreads, 0, st>>>(p);
+  }
+  return cudaGetLastError() == cudaSuccess ? SSKIP_OK : SSKIP_ERR_CUDA;
+}
+
+SSKIP_API int sskip_attn_decode_paged(const void* q, const void* k_pages, const void* v_pages,
+                                      const int* block_table, const int* seqlens, void* o,
+                                      float* lse, int kv_format, int B, int Hq, int Hkv,
+                                      int num_pages, int page_size, int max_pages, int d,
+                                      float sm_scale, float threshold_scale_factor, int num_splits,
+                                      void* workspace, size_t workspace_bytes,
+                                      unsigned long long* skip_count, uint8_t* tile_state,
+                                      void* stream) {
+  if (!q || !seqlens || !o || !lse) return SSKIP_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(o) || misaligned(seqlens, 3) || misaligned(lse, 3) ||
+      misaligned(workspace, 255) || misaligned(skip_count, 7))
+    return SSKIP_ERR_INVALID_ARG;
+  const int rc = paged_check(k_pages, v_pages, block_table, kv_format, num_pages, page_size,
+                             max_pages, B, Hkv, d);
+  if (rc != SSKIP_OK) return rc;
+  if (Hq < 1 || Hq % Hkv != 0 || num_splits < 1) return SSKIP_ERR_INVALID_ARG;
+  if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return SSKIP_ERR_INVALID_ARG;
+  if (!(threshold_scale_factor >= 0.f) || !std::isfinite(threshold_scale_factor))
+    return SSKIP_ERR_INVALID_ARG;
+  const int G = Hq / Hkv;
+  if (B > 65535 || Hkv > 65535 || num_splits > 64 || (long long)B * Hq > 0x7FFFFFFFll)
+    return SSKIP_ERR_UNSUPPORTED;
+  if (G != 1 && G != 2 && G != 4 && G != 8) return SSKIP_ERR_UNSUPPORTED;
+  if (num_splits > 1 &&
+      (!workspace || workspace_bytes < sskip_attn_decode_workspace_size(B, Hq, d, num_splits)))
+    return SSKIP_ERR_INVALID_ARG;
+
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const size_t rows = (size_t)B * Hq * num_splits;
+  PagedDecodeParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.seqlens = seqlens;
+  p.c = paged_rows(const_cast<void*>(k_pages), const_cast<void*>(v_pages), block_table, num_pages,
+                   page_size, max_pages, B, Hkv);
+  if (num_splits > 1) {
+    p.o_part = static_cast<float*>(workspace);
+    p.lse_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + align256(rows * d * 4));
+  }
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.counts = skip_count;
+  p.tile_state = tile_state;
+  p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.G = G; p.S = num_splits;
+  p.n_k_max = (int)(((long long)max_pages * page_size + kPgTile - 1) / kPgTile);
+  p.scale_log2 = (float)((double)sm_scale * 1.4426950408889634);
+  p.tsf = threshold_scale_factor;
+  CUtensorMap mk{}, mv{};
+  if (kv_format == SSKIP_KV_BF16) {
+    const long long n = (long long)num_pages * Hkv * page_size;
+    const int box = std::min(page_size, kPgTile);
+    if (!make_page_map(&mk, k_pages, d, n, box) || !make_page_map(&mv, v_pages, d, n, box))
+      return SSKIP_ERR_CUDA;
+  }
+  if (skip_count && cudaMemsetAsync(skip_count, 0, 2 * sizeof(unsigned long long), st) != cudaSuccess)
+    return SSKIP_ERR_CUDA;
+  if (tile_state &&
+      cudaMemsetAsync(tile_state, 0, (size_t)B * Hkv * p.n_k_max, st) != cudaSuccess)
+    return SSKIP_ERR_CUDA;
+  if (kv_format == SSKIP_KV_INT4)
+    return d == 128 ? launch_decode_paged<128, true>(mk, mv, p, st)
+                    : launch_decode_paged<64, true>(mk, mv, p, st);
+  return d == 128 ? launch_decode_paged<128, false>(mk, mv, p, st)
+                  : launch_decode_paged<64, false>(mk, mv, p, st);
 }

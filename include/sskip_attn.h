@@ -31,8 +31,8 @@
  *  - `stream` is a cudaStream_t passed as void* (NULL = legacy default stream).
  *    Every device call is asynchronous on that stream and allocates no device
  *    memory.  sskip_attn_prefill_host also creates two copy streams once per
- *    device and a few events per call.  sskip_calibrate_factor and
- *    sskip_hilbert3d_order are host-only and synchronous.
+ *    device and a few events per call.  sskip_calibrate_factor,
+ *    sskip_hilbert3d_order and sskip_rope_freqs are host-only and synchronous.
  *  - The return value reports argument validation and launch errors
  *    synchronously (sskip_status).  Errors found on the device while a kernel
  *    runs (a bounded wait that ran out, an out-of-range device-side length
@@ -379,12 +379,164 @@ int sskip_permute_rows(const void* src, void* dst, const int32_t* idx, long long
                        int row_bytes, int scatter, void* stream);
 
 /*
+ * The paged key/value cache
+ * -------------------------
+ * Pages of page_size tokens (16, 32, 64, 128 or 256) live in two pools, one
+ * for keys and one for values; a sequence's page number i stands in row b of
+ * the block table, at column i: its token at position p is row p % page_size
+ * of page block_table[b, p / page_size].  Pages may stand in any order, and
+ * several sequences may share a page for READING (a common prefix).
+ *
+ *   block_table [B, max_pages] int32 on the device; entries past a sequence's
+ *     last page are never read.
+ *   k_pages, v_pages: num_pages pages of sskip_kv_page_bytes(...) bytes each,
+ *     16-byte aligned, in one of two formats:
+ *   SSKIP_KV_BF16  [num_pages, Hkv, page_size, d] bf16.
+ *   SSKIP_KV_INT4  [num_pages, Hkv, page_size / 16] records of 8 d + 2 d
+ *     bytes, 16 rows each.  32 neighbouring values of a row share
+ *       mn = min, rounded down to bf16,   sc = (max - mn) / 15, rounded up to bf16,
+ *       n  = rint((x - mn) / sc), ties to even, clamped to 0 .. 15,
+ *     and stand for sc n + mn.  A group that holds a NaN or an infinity reads
+ *     back as NaN.  The order of the codes, then of the [16][d / 32] bf16
+ *     pairs (sc, mn), is the one the decode kernel's tensor-core fragments
+ *     want; with r = row % 16:
+ *       keys:   byte r d / 2 + 4 ((m % 4) (d / 32) + m / 4) starts the 32-bit
+ *               word of values 8 m .. 8 m + 7: value 8 m + e is nibble
+ *               e / 2 + 4 (e % 2);
+ *       values: byte ((r / 8) 32 + 4 g + (r / 2) % 4) (d / 8) + 4 a + 2 (r % 2)
+ *               starts the 16-bit unit of values 32 a + 4 g .. 32 a + 4 g + 3,
+ *               in nibbles 0 .. 3;
+ *       scales: byte 8 d + 4 (r (d / 32) + a) holds sc, then mn, of group a.
+ * Supported: d in {64, 128}; max_pages * page_size and num_pages * Hkv *
+ * page_size below 2^31.  Indices in device memory are checked by the kernels:
+ * a bad one latches SSKIP_ERR_INVALID_ARG (see sskip_get_status) and nothing
+ * outside the pools is touched.
+ */
+typedef enum { SSKIP_KV_BF16 = 0, SSKIP_KV_INT4 = 1 } sskip_kv_format;
+
+/* Bytes of one page of keys (or of values); 0 for an unsupported shape. */
+size_t sskip_kv_page_bytes(int kv_format, int Hkv, int page_size, int d);
+
+/*
+ * Rotation frequencies.  Pair i of rot_dim / 2 turns by
+ * base^(-2 i / rot_dim) radians a position, scaled for contexts longer than
+ * the trained one (original_len) by `scaling`:
+ *   SSKIP_ROPE_PLAIN   not at all;
+ *   SSKIP_ROPE_LINEAR  every frequency / factor (position interpolation);
+ *   SSKIP_ROPE_BANDS   pairs that make fewer than slow_turns turns over
+ *     original_len by 1 / factor, those with more than fast_turns unchanged, a
+ *     linear blend in the turns between;
+ *   SSKIP_ROPE_YARN    the same blend linear in the pair's index, between the
+ *     (rounded) pairs of fast_turns and slow_turns, and the factor
+ *     0.1 ln(factor) + 1 on cosine and sine (Peng et al., "YaRN", 2023).
+ * HOST call, no CUDA.  turns[i] (host, [rot_dim / 2]) is the frequency in
+ * units of 2^-64 turn per position; the caller copies the table to the device
+ * once.  A position times it, modulo 2^64, is the angle modulo one turn, so
+ * angles are exact however far the position.  attn_factor (out, may be NULL).
+ */
+typedef enum {
+    SSKIP_ROPE_PLAIN = 0,
+    SSKIP_ROPE_LINEAR = 1,
+    SSKIP_ROPE_BANDS = 2,
+    SSKIP_ROPE_YARN = 3
+} sskip_rope_scaling;
+
+int sskip_rope_freqs(int rot_dim, double base, int scaling, double factor, double slow_turns,
+                     double fast_turns, double original_len, uint64_t* turns,
+                     double* attn_factor);
+
+/*
+ * From a layer's projections to its attention, in one pass: per query and key
+ * head an optional RMS norm, the rotation by position, then the rows written
+ * where they are read next.
+ *
+ *   q [T, Hq, d], k, v [T, Hkv, d] bf16: T tokens, heads packed, q_stride (and
+ *     so on) elements between tokens, a multiple of 8: the three may be slices
+ *     of one projection.  Hq = 0 (q, q_out, q_weight NULL) or Hkv = 0 (k, v,
+ *     their outputs, the pages and k_weight NULL) leaves that side out.
+ *   seq_ids, positions [T] int32 on the device: the token's row of the block
+ *     table and its position.  seq_ids[t] < 0 is padding: nothing is read or
+ *     written for that token, its output rows stay as they were.  seq_ids may
+ *     be NULL without pages, positions also when rot_dim = 0.
+ *   q_weight, k_weight [d] bf16, or NULL for no norm:
+ *     x rsqrt(mean over d of x^2 + eps) weight, in fp32.
+ *   turns [rot_dim / 2] on the device (sskip_rope_freqs), rot_dim a multiple
+ *     of 16, 0 .. d: the first rot_dim values of a head turn, in pairs
+ *     (i, i + rot_dim / 2), or (2 i, 2 i + 1) with interleaved != 0:
+ *     (a, b) -> (a cos - b sin, a sin + b cos), both times attn_factor.
+ *   q_out [T / out_len, Hq, out_len, d], k_out, v_out [T / out_len, Hkv,
+ *     out_len, d] bf16: out_len = 1 is the decode's layout (one token a
+ *     sequence), out_len = L the prefill's [B, H, L, d].  T % out_len == 0.
+ *     k_out and v_out are optional (both or neither) when there are pages.
+ *   k_pages, v_pages: the cache the rows are appended to (both or neither).
+ *     A token whose sequence, position or page is out of range is latched and
+ *     left out entirely.  No two tokens of a call, and no two calls in flight
+ *     at a time, may write the same position of a page.
+ *
+ * Norm and rotation run in fp32 with one rounding at the end, to bf16 or (for
+ * SSKIP_KV_INT4) from fp32 to the 4-bit form.  No output may overlap an input
+ * or another output.  T = 0 is a call that does nothing.
+ */
+int sskip_kv_append(const void* q, const void* k, const void* v, long long q_stride,
+                    long long k_stride, long long v_stride, const int* seq_ids,
+                    const int* positions, const void* q_weight, const void* k_weight, float eps,
+                    const uint64_t* turns, int rot_dim, int interleaved, float attn_factor,
+                    void* q_out, void* k_out, void* v_out, int out_len, void* k_pages,
+                    void* v_pages, const int* block_table, int kv_format, int num_pages,
+                    int page_size, int max_pages, int T, int B, int Hq, int Hkv, int d,
+                    void* stream);
+
+/*
+ * Rows of the cache back as bf16: for T tokens (seq_ids, positions as above;
+ * padding and out-of-range tokens leave their rows as they were), keys and
+ * values into k_out, v_out [T / out_len, Hkv, out_len, d].  A cached prefix for
+ * the prefill, a contiguous cache for sskip_attn_decode, an export.  4-bit
+ * values are computed in fp32 and rounded once to bf16.  The same token may be
+ * asked for several times.  T = 0 does nothing.
+ */
+int sskip_kv_gather(const void* k_pages, const void* v_pages, const int* block_table,
+                    const int* seq_ids, const int* positions, void* k_out, void* v_out,
+                    int out_len, int kv_format, int num_pages, int page_size, int max_pages, int T,
+                    int B, int Hkv, int d, void* stream);
+
+/*
+ * Decode over a paged cache: sskip_attn_decode's rule (decode tiles of 64 keys
+ * and the G query heads of a kv head, one joint decision a tile, splits with
+ * their own running maximum, log-sum-exp merge; t_b =
+ * threshold_scale_factor / seqlens[b]) on keys and values that stand in pages,
+ * in either format.
+ *
+ *   q [B, Hq, d], o [B, Hq, d] bf16, lse [B, Hq] fp32 natural log.
+ *   seqlens [B] int32 on the device, 0 <= seqlens[b] <= max_pages * page_size.
+ *     0 gives O = 0 and lse = -inf (a padded batch entry).  Another length is
+ *     latched and clamped; a page outside the pool is latched and read as page
+ *     0, the outputs of that sequence then mean nothing.  Rows at or beyond
+ *     seqlens[b] may hold anything, NaN included.
+ *   num_splits 1 .. 64; G in {1, 2, 4, 8}; the tile is 64 keys.
+ *   workspace: sskip_attn_decode_workspace_size(B, Hq, d, num_splits) bytes,
+ *     256-byte aligned; may be NULL with num_splits = 1.  Calls in flight at a
+ *     time (two streams, two captured graphs) need one each.
+ *   skip_count: optional device uint64[2] = {skipped, visited} tiles.
+ *   tile_state: optional [B, Hkv, ceil(max_pages * page_size / 64)] uint8:
+ *     0 not visited, 1 kept, 2 skipped.
+ * P is rounded to bf16 for its product with V, the row sum is not; in the
+ * 4-bit form the value's scale joins P before that rounding.
+ */
+int sskip_attn_decode_paged(const void* q, const void* k_pages, const void* v_pages,
+                            const int* block_table, const int* seqlens, void* o, float* lse,
+                            int kv_format, int B, int Hq, int Hkv, int num_pages, int page_size,
+                            int max_pages, int d, float sm_scale, float threshold_scale_factor,
+                            int num_splits, void* workspace, size_t workspace_bytes,
+                            unsigned long long* skip_count, uint8_t* tile_state, void* stream);
+
+/*
  * Synchronises `stream`, then returns and clears the current device's status
  * word: SSKIP_OK, or the first device-side error latched since the last call
  * (SSKIP_ERR_TIMEOUT when a bounded wait inside a kernel ran out: the kernel
  * then abandoned its work, waited out its own copies in flight and left its
- * outputs undefined; SSKIP_ERR_INVALID_ARG when a decode length or a permute
- * index held in device memory was out of range).  Returns SSKIP_ERR_CUDA if
+ * outputs undefined; SSKIP_ERR_INVALID_ARG when a decode length, a permute
+ * index, or a sequence, position or page of the paged cache held in device
+ * memory was out of range).  Returns SSKIP_ERR_CUDA if
  * the synchronisation itself failed.
  */
 int sskip_get_status(void* stream);
