@@ -1,5 +1,5 @@
-// decode_paged_sm100.cuh -- split-KV Skip-Softmax decode over a paged cache,
-// in bf16 or in 4 bits.
+// decode_paged_sm100.cuh -- split-KV Skip-Softmax decode over a paged cache:
+// bf16 pages, and what the 4-bit kernel (decode_paged4_sm100.cuh) shares.
 //
 // The rule is that of the contiguous decode: a decode tile is 64 keys and the
 // G = Hq / Hkv query heads of one kv head, the heads take one joint decision,
@@ -14,8 +14,7 @@
 // it empty), and one 8x8 transpose of the packed P turns the first product's
 // result into the second's operand.  Each warp keeps O^T of its own keys in
 // registers; the warps merge once per split.  (tcgen05 has no use here: the
-// kernel is bound by HBM, and the 4-bit form wants its operands in registers,
-// where the codes are widened.)
+// kernel is bound by HBM.)
 //
 // Without a threshold (SKIP = false) K and V tiles are fetched together, no
 // warp ever waits for another, and the softmax reference of a warp moves only
@@ -49,11 +48,11 @@ constexpr int kPgWarps = 4;                          // consumer warps
 constexpr int kPgThreads = (kPgWarps + 1) * 32;
 constexpr int kPgLag = 2;                            // P.V runs this many tiles behind the vote
 
-template <int D, bool Q4>
+template <int D>
 struct PagedCfg {
-  static constexpr int kTileBytes = Q4 ? 4 * Kv4<D>::kRecord : kPgTile * D * 2;
-  static constexpr int kStages = Q4 ? 6 : (D == 128 ? 3 : 6);  // of K and of V
-  static constexpr int kCtas = Q4 ? 3 : 2;                      // per SM
+  static constexpr int kTileBytes = kPgTile * D * 2;
+  static constexpr int kStages = D == 128 ? 3 : 6;  // of K and of V
+  static constexpr int kCtas = 2;                   // per SM
   static constexpr int kK = 0;
   static constexpr int kV = kK + kStages * kTileBytes;
   static constexpr int kMax = kV + kStages * kTileBytes;        // [2][8][W] fp32
@@ -92,44 +91,118 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The four pairs of a 4-bit word as bf16 pairs n - 8: the code under the
-// exponent of 128 is 128 + n, and taking 136 away is exact.
-__device__ __forceinline__ void widen_codes(uint32_t w, uint32_t (&r)[4]) {
-  const __nv_bfloat162 bias = __halves2bfloat162(__ushort_as_bfloat16(0x4308),
-                                                 __ushort_as_bfloat16(0x4308));
+// What a split without tiles leaves: nothing for the merge to weigh, or (with
+// one split) the empty sequence's O = 0 and lse = -inf.
+template <int D>
+__device__ __forceinline__ void paged_empty_split(const PagedDecodeParams& p, size_t head0,
+                                                  int split, int tid, int threads) {
+  if (p.S == 1) {
+    for (int i = tid; i < p.G * D; i += threads) p.o[head0 * D + i] = __float2bfloat16_rn(0.f);
+    if (tid < p.G) p.lse[head0 + tid] = -INFINITY;
+  } else if (tid < p.G) {
+    p.lse_part[(head0 + tid) * p.S + split] = -INFINITY;
+  }
+}
+
+// How the lanes of a warp share a tile's copies.  A tile of 64 rows comes in
+// 64 / rows copies (one when a page holds a tile), a bf16 row of 128 values in
+// two 128-byte-wide halves, and K and V tiles may go out together: every copy
+// is one lane's, so issuing a tile costs the warp one pass through the code.
+struct PagedLane {
+  int shift, rows, row_shift, npt;  // page size, rows of a copy, copies of a tile
+  int sub, half, val;               // this lane's copy, half, and K (0) or V (1)
+  __device__ __forceinline__ PagedLane(const PagedRows& c, int lane) {
+    shift = c.page_shift;
+    row_shift = min(shift, 6);
+    rows = 1 << row_shift;
+    npt = kPgTile >> row_shift;
+    sub = lane & 3;
+    half = (lane >> 2) & 1;
+    val = (lane >> 3) & 1;
+  }
+  // Copies of tile j that hold a key: those behind the last one are not fetched.
+  __device__ __forceinline__ int copies(int j, int len) const {
+    return min(npt, (len - j * kPgTile + rows - 1) >> row_shift);
+  }
+  // Row of the pools (pages, heads and rows flattened) of this lane's copy.
+  __device__ __forceinline__ long long row(int j, int page, int Hkv, int kvh) const {
+    const int off = (j * kPgTile + sub * rows) & ((1 << shift) - 1);
+    return (((long long)page * Hkv + kvh) << shift) + off;
+  }
+  __device__ __forceinline__ int slot(int j) const { return (j * kPgTile + sub * rows) >> shift; }
+};
+
+// A page outside the pool is latched and read as page 0.
+__device__ __forceinline__ int paged_checked(const PagedRows& c, int page) {
+  if (page >= 0 && page < c.num_pages) return page;
+  latch_status(kStatusInvalidArg);
+  return 0;
+}
+
+struct PagedCell {
+  int d;
+  float x;
+};
+
+// Merge W warps' O^T, references m (log2 units) and per-lane row sums l of
+// heads 2 c, 2 c + 1, and write the split, or the result when it is the only
+// one.  cell(mt, i): column and value of accumulator i of row tile mt.  red:
+// W * 8 * (D + 4) floats of shared memory that nothing else uses any more.
+template <int D, int W, typename Cell>
+__device__ __forceinline__ void paged_merge_warps(const PagedDecodeParams& p, float* red,
+                                                  float2* stat, size_t head0, int split, int tid,
+                                                  const float (&m)[2], float (&l)[2], Cell cell) {
+  constexpr int RS = D + 4;  // row stride of the merge buffer: spreads the banks
+  const int warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t x = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-    const __nv_bfloat162 y = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), bias);
-    r[i] = *reinterpret_cast<const uint32_t*>(&y);
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
+#pragma unroll
+  for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const PagedCell e = cell(mt, i);
+      red[(warp * 8 + 2 * c + (i & 1)) * RS + e.d] = e.x;
+    }
+  if (g == 0) {
+    stat[warp * 8 + 2 * c] = make_float2(m[0], l[0]);
+    stat[warp * 8 + 2 * c + 1] = make_float2(m[1], l[1]);
+  }
+  named_bar_sync(1, W * 32);
+  for (int i = tid; i < p.G * D; i += W * 32) {
+    const int h = i / D, d = i % D;
+    float2 st[W];
+    float mx = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      st[w] = stat[w * 8 + h];
+      mx = fmaxf(mx, st[w].x);
+    }
+    float sum = 0.f, o = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float e = st[w].x == -INFINITY ? 0.f : ex2_approx(st[w].x - mx);
+      sum = fmaf(e, st[w].y, sum);
+      o = fmaf(e, red[(w * 8 + h) * RS + d], o);
+    }
+    const float lse = (mx + __log2f(sum)) * 0.69314718055994531f;
+    if (p.S == 1) {
+      p.o[(head0 + h) * D + d] = __float2bfloat16_rn(o / sum);
+      if (d == 0) p.lse[head0 + h] = lse;
+    } else {
+      p.o_part[((head0 + h) * p.S + split) * D + d] = o / sum;
+      if (d == 0) p.lse_part[(head0 + h) * p.S + split] = lse;
+    }
   }
 }
 
-// n words of shared memory, n * 4 bytes aligned (n = 2 or 4).
-template <int N>
-__device__ __forceinline__ void lds_words(uint32_t (&w)[N], const uint8_t* p) {
-  if constexpr (N == 4) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-  } else {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    w[0] = v.x; w[1] = v.y;
-  }
-}
-
-// (sc, mn) of a word -> the scale of n - 8 and what 0 stands for there.
-__device__ __forceinline__ void kv4_affine(uint32_t w, float& sc, float& zero) {
-  sc = __uint_as_float(w << 16);
-  zero = fmaf(8.f, sc, __uint_as_float(w & 0xFFFF0000u));
-}
-
-template <int D, bool Q4, bool SKIP>
-__global__ void __launch_bounds__(kPgThreads, PagedCfg<D, Q4>::kCtas)
+template <int D, bool SKIP>
+__global__ void __launch_bounds__(kPgThreads, PagedCfg<D>::kCtas)
     decode_paged_kernel(const __grid_constant__ CUtensorMap map_k,
                         const __grid_constant__ CUtensorMap map_v, const PagedDecodeParams p) {
-  using C = PagedCfg<D, Q4>;
+  using C = PagedCfg<D>;
   constexpr int NS = C::kStages;
-  constexpr int NG = D / 32;   // 4-bit groups of a row
   constexpr int MT = D / 16;   // 16-row tiles of O^T
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -150,14 +223,8 @@ __global__ void __launch_bounds__(kPgThreads, PagedCfg<D, Q4>::kCtas)
   const int ntiles = max(0, min(n_k, j0 + c_per) - j0);
   const size_t head0 = (size_t)b * p.Hq + (size_t)kvh * p.G;
 
-  if (ntiles == 0) {  // an empty split contributes nothing to the merge
-    if (p.S == 1) {
-      for (int i = tid; i < p.G * D; i += kPgThreads)
-        p.o[head0 * D + i] = __float2bfloat16_rn(0.f);
-      if (tid < p.G) p.lse[head0 + tid] = -INFINITY;
-    } else if (tid < p.G) {
-      p.lse_part[(head0 + tid) * p.S + split] = -INFINITY;
-    }
+  if (ntiles == 0) {
+    paged_empty_split<D>(p, head0, split, tid, kPgThreads);
     return;
   }
 
@@ -181,80 +248,54 @@ __global__ void __launch_bounds__(kPgThreads, PagedCfg<D, Q4>::kCtas)
   }
   __syncthreads();
 
-  // A tile's pages: one when a page holds a tile, else 64 / P, of which those
-  // behind the last key are not fetched.
-  const int P = 1 << p.c.page_shift;
-  const int rows = min(P, kPgTile);            // of one copy
-  auto tile_copies = [&](int j) { return min(kPgTile / rows, (Lb - j * kPgTile + rows - 1) / rows); };
-  const uint32_t copy_bytes = (uint32_t)rows * (C::kTileBytes / kPgTile);
-
-  // One elected thread: the copies of tile j (of K or of V) into ring slot s.
-  auto fetch = [&](bool val, int j, int s, const int* page) {
+  // A whole warp: tile j's copies of K (val = 0) or V into ring slot s; each
+  // lane brings the page of its copy.
+  const PagedLane ln(p.c, lane);
+  const uint32_t copy_bytes = (uint32_t)ln.rows * 128;  // of one half
+  auto fetch = [&](int val, bool on, int j, int s, int page) {
     const uint32_t bar = val ? vfull(s) : kfull(s);
     const uint32_t dst = (val ? v_smem : k_smem) + s * C::kTileBytes;
-    const int n = tile_copies(j);
-    if (!dev_check(j < n_k && n >= 1 && n <= 4 && s < NS)) {
-      mbar_arrive(bar);
-      return;
+    const int n = ln.copies(j, Lb);
+    const bool ok = dev_check(j < n_k && n >= 1 && n <= 4 && s < NS);
+    if (on && ln.sub == 0 && ln.half == 0) {
+      if (ok) mbar_arrive_expect_tx(bar, n * copy_bytes * (D / 64));
+      else mbar_arrive(bar);  // the phase completes without data
     }
-    mbar_arrive_expect_tx(bar, n * copy_bytes);
-    const int off = (j * kPgTile) & (P - 1);
-    for (int i = 0; i < n; ++i) {
-      if constexpr (Q4) {
-        const uint8_t* base = val ? p.c.v_pages : p.c.k_pages;
-        const size_t rec = (((size_t)page[i] * p.Hkv + kvh) << (p.c.page_shift - 4)) + (off >> 4);
-        bulk_load(dst + i * copy_bytes, base + rec * Kv4<D>::kRecord, copy_bytes, bar);
-      } else {
-        const int y = ((page[i] * p.Hkv + kvh) << p.c.page_shift) + off;
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h)
-          tma_load_2d(dst + h * (kPgTile * 128) + i * rows * 128, val ? &map_v : &map_k, bar,
-                      h * 64, y);
-      }
-    }
+    __syncwarp();
+    if (on && ok && ln.sub < n && ln.half < D / 64)
+      tma_load_2d(dst + ln.half * (kPgTile * 128) + ln.sub * copy_bytes, val ? &map_v : &map_k, bar,
+                  ln.half * 64, (int)ln.row(j, page, p.Hkv, kvh));
   };
 
   if (warp == kPgWarps) {
     // ------------------------------------------------------------ producer
     const int* table = p.c.block_table + (size_t)b * p.c.max_pages;
-    int issued = 0;
+    const int val = SKIP ? 0 : ln.val;
+    const bool mine = lane < (SKIP ? 8 : 16) && ln.half < D / 64;
+    // The page of this lane's copy of a tile, loaded a tile ahead.
+    auto page_of = [&](int j) {
+      return mine && j < n_k && ln.sub < ln.copies(j, Lb) ? __ldg(table + ln.slot(j)) : 0;
+    };
+    int issued = 0, s = 0, par = 1, next = page_of(j0);
     bool ok = true;
-    for (int t = 0; t < ntiles && ok; ++t) {
-      const int j = j0 + t, s = t % NS;
-      const int slot0 = (j * kPgTile) >> p.c.page_shift;
-      int page[4];
-      const int n = tile_copies(j);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        page[i] = i < n ? __ldg(table + slot0 + i) : 0;
-        if (page[i] < 0 || page[i] >= p.c.num_pages) {
-          if (lane == 0) latch_status(kStatusInvalidArg);
-          page[i] = 0;
-        }
-      }
-      if (t >= NS) {
-        ok = mbar_wait(kfree(s), ((t / NS) - 1) & 1, abort_flag);
-        if (ok && !SKIP) ok = mbar_wait(vfree(s), ((t / NS) - 1) & 1, abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
-      }
-      if (ok && lane == 0) {
-        if (SKIP) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) ids[s * 4 + i] = page[i];
-        }
-        fetch(false, j, s, page);
-        if (!SKIP) fetch(true, j, s, page);
-        issued = t + 1;
-      }
+    for (int t = 0; t < ntiles; ++t) {
+      const int j = j0 + t, page = paged_checked(p.c, next);
+      next = page_of(j + 1);
+      if (t >= NS) ok = mbar_wait(val ? vfree(s) : kfree(s), par, abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (SKIP && mine && ln.half == 0) ids[s * 4 + ln.sub] = page;
+      __syncwarp();
+      fetch(val, mine, j, s, page);
+      issued = t + 1;
+      if (++s == NS) { s = 0; par ^= 1; }
     }
     __syncthreads();
     if (*abort_flag && lane == 0) {  // wait out the copies in flight before the CTA exits
       int no_abort = 0;
-      for (int s = 0; s < NS; ++s)
-        if (issued > s) {
-          const int last = s + (issued - 1 - s) / NS * NS;
-          mbar_wait(kfull(s), (last / NS) & 1, &no_abort);
-          if (!SKIP) mbar_wait(vfull(s), (last / NS) & 1, &no_abort);
+      for (int i = 0; i < NS; ++i)
+        if (issued > i) {
+          mbar_wait(kfull(i), ((issued - 1 - i) / NS) & 1, &no_abort);
+          if (!SKIP) mbar_wait(vfull(i), ((issued - 1 - i) / NS) & 1, &no_abort);
         }
     }
     return;
@@ -264,87 +305,42 @@ __global__ void __launch_bounds__(kPgThreads, PagedCfg<D, Q4>::kCtas)
   const int g = lane >> 2, c = lane & 3;
   // Q^T fragments: head g, the d's that the K fragments hold at this lane.
   uint32_t qf[MT][2];
-  float qsum[2][NG];  // sum of q over a group, heads 2 c and 2 c + 1 (4-bit)
   {
     const __nv_bfloat16* q = p.q + (head0 + g) * D;
 #pragma unroll
     for (int kt = 0; kt < MT; ++kt)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int d = Q4 ? (kt >> 1) * 32 + 8 * c + 2 * ((kt & 1) * 2 + i) : kt * 16 + i * 8 + 2 * c;
+        const int d = kt * 16 + i * 8 + 2 * c;
         qf[kt][i] = g < p.G ? *reinterpret_cast<const uint32_t*>(q + d) : 0u;
       }
-    if constexpr (Q4) {
-#pragma unroll
-      for (int gr = 0; gr < NG; ++gr) {
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t w = qf[2 * gr + (i >> 1)][i & 1];
-          s += __uint_as_float(w << 16) + __uint_as_float(w & 0xFFFF0000u);
-        }
-        s += __shfl_xor_sync(0xffffffffu, s, 1);
-        s += __shfl_xor_sync(0xffffffffu, s, 2);
-        qsum[0][gr] = __shfl_sync(0xffffffffu, s, 8 * c);
-        qsum[1][gr] = __shfl_sync(0xffffffffu, s, 8 * c + 4);
-      }
-    }
   }
   float* wmax = reinterpret_cast<float*>(smem + C::kMax);
   const bool t_positive = SKIP;
   const float log2_t = SKIP ? (float)log2((double)p.tsf / (double)Lb) : -INFINITY;
 
   float acc[MT][4];                 // O^T
-  float zacc[NG][2];                // sum of p times the groups' zeros (4-bit)
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // heads 2 c, 2 c + 1
 #pragma unroll
   for (int i = 0; i < MT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-#pragma unroll
-  for (int i = 0; i < NG; ++i) zacc[i][0] = zacc[i][1] = 0.f;
 
   // Scores of this warp's 16 keys of tile t, in log2 units: s[0..1] key g,
   // s[2..3] key g + 8, heads 2 c and 2 c + 1; keys past the end -> -inf.
   auto scores = [&](int t, float (&s)[4]) {
     const int valid = Lb - (j0 + t) * kPgTile - warp * 16;  // of the 16
     const uint8_t* tile = smem + C::kK + (t % NS) * C::kTileBytes;
-    if constexpr (Q4) {
-      const uint8_t* rec = tile + warp * Kv4<D>::kRecord;
-      uint32_t wa[NG], wb[NG], pa[NG], pb[NG];
-      lds_words<NG>(wa, rec + g * (D / 2) + c * NG * 4);
-      lds_words<NG>(wb, rec + (g + 8) * (D / 2) + c * NG * 4);
-      lds_words<NG>(pa, rec + Kv4<D>::kCodes + g * NG * 4);
-      lds_words<NG>(pb, rec + Kv4<D>::kCodes + (g + 8) * NG * 4);
-      s[0] = s[1] = s[2] = s[3] = 0.f;
+    const uint32_t base = smem_u32(tile) + warp * 16 * 128;
+    const int row = (lane & 7) + ((lane >> 3) & 1) * 8, ch = lane >> 4;
+    float x[2][4] = {};
 #pragma unroll
-      for (int gr = 0; gr < NG; ++gr) {
-        uint32_t a[4], e[4];
-        widen_codes(wa[gr], a);
-        widen_codes(wb[gr], e);
-        float x[4] = {0.f, 0.f, 0.f, 0.f};
-        mma16816(x, a[0], e[0], a[1], e[1], qf[2 * gr][0], qf[2 * gr][1]);
-        mma16816(x, a[2], e[2], a[3], e[3], qf[2 * gr + 1][0], qf[2 * gr + 1][1]);
-        float sa, za, sb, zb;
-        kv4_affine(pa[gr], sa, za);
-        kv4_affine(pb[gr], sb, zb);
-        s[0] = fmaf(sa, x[0], fmaf(za, qsum[0][gr], s[0]));
-        s[1] = fmaf(sa, x[1], fmaf(za, qsum[1][gr], s[1]));
-        s[2] = fmaf(sb, x[2], fmaf(zb, qsum[0][gr], s[2]));
-        s[3] = fmaf(sb, x[3], fmaf(zb, qsum[1][gr], s[3]));
-      }
-    } else {
-      const uint32_t base = smem_u32(tile) + warp * 16 * 128;
-      const int row = (lane & 7) + ((lane >> 3) & 1) * 8, ch = lane >> 4;
-      float x[2][4] = {};
-#pragma unroll
-      for (int kt = 0; kt < MT; ++kt) {
-        const int chunk = kt * 2 + ch;
-        uint32_t a[4];
-        ldsm4(base + (chunk >> 3) * (kPgTile * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4), a);
-        mma16816(x[kt & 1], a[0], a[1], a[2], a[3], qf[kt][0], qf[kt][1]);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] = x[0][i] + x[1][i];
+    for (int kt = 0; kt < MT; ++kt) {
+      const int chunk = kt * 2 + ch;
+      uint32_t a[4];
+      ldsm4(base + (chunk >> 3) * (kPgTile * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4), a);
+      mma16816(x[kt & 1], a[0], a[1], a[2], a[3], qf[kt][0], qf[kt][1]);
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = x[0][i] + x[1][i];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       s[i] = (g + (i >> 1) * 8 < valid) ? s[i] * p.scale_log2 : -INFINITY;
@@ -359,65 +355,34 @@ __global__ void __launch_bounds__(kPgThreads, PagedCfg<D, Q4>::kCtas)
       for (int i = 0; i < MT; ++i) {
         acc[i][0] *= a0; acc[i][1] *= a1; acc[i][2] *= a0; acc[i][3] *= a1;
       }
-#pragma unroll
-      for (int i = 0; i < NG; ++i) { zacc[i][0] *= a0; zacc[i][1] *= a1; }
     }
     if (valid <= 0) return;
-    if constexpr (Q4) {
-      const uint8_t* rec = tile + warp * Kv4<D>::kRecord;
-      uint32_t w0[NG], w1[NG], pa[NG], pb[NG];
-      lds_words<NG>(w0, rec + lane * NG * 4);
-      lds_words<NG>(w1, rec + (32 + lane) * NG * 4);
-      lds_words<NG>(pa, rec + Kv4<D>::kCodes + g * NG * 4);
-      lds_words<NG>(pb, rec + Kv4<D>::kCodes + (g + 8) * NG * 4);
+    if (valid < 16) {  // rows behind the last key: P is 0 there, V may be NaN
+      for (int i = lane; i < (16 - valid) * 8; i += 32)
 #pragma unroll
-      for (int gr = 0; gr < NG; ++gr) {
-        float sa, za, sb, zb;
-        kv4_affine(pa[gr], sa, za);
-        kv4_affine(pb[gr], sb, zb);
-        // Behind the last key the record holds what an earlier sequence left:
-        // its codes are numbers, its scales need not be.
-        if (g >= valid) sa = za = 0.f;
-        if (g + 8 >= valid) sb = zb = 0.f;
-        zacc[gr][0] = fmaf(pr[0], za, fmaf(pr[2], zb, zacc[gr][0]));
-        zacc[gr][1] = fmaf(pr[1], za, fmaf(pr[3], zb, zacc[gr][1]));
-        // The scale joins P before its rounding to bf16 (2^-9 of the product).
-        const uint32_t b0 = transpose8x8(pack_bf16x2(pr[0] * sa, pr[1] * sa));
-        const uint32_t b1 = transpose8x8(pack_bf16x2(pr[2] * sb, pr[3] * sb));
-        uint32_t a[4], e[4];
-        widen_codes(w0[gr], a);
-        widen_codes(w1[gr], e);
-        mma16816(acc[2 * gr], a[0], a[1], e[0], e[1], b0, b1);
-        mma16816(acc[2 * gr + 1], a[2], a[3], e[2], e[3], b0, b1);
-      }
-    } else {
-      if (valid < 16) {  // rows behind the last key: P is 0 there, V may be NaN
-        for (int i = lane; i < (16 - valid) * 8; i += 32)
+        for (int h = 0; h < D / 64; ++h)
+          *reinterpret_cast<uint4*>(tile + h * (kPgTile * 128) +
+                                    (warp * 16 + valid + (i >> 3)) * 128 + (i & 7) * 16) =
+              make_uint4(0, 0, 0, 0);
+      __syncwarp();
+    }
+    // P is rounded to bf16 for the product (2^-9 of each weight); l is not.
+    const uint32_t b0 = transpose8x8(pack_bf16x2(pr[0], pr[1]));
+    const uint32_t b1 = transpose8x8(pack_bf16x2(pr[2], pr[3]));
+    const uint32_t base = smem_u32(tile) + warp * 16 * 128;
+    const int row = (lane & 7) + (lane >> 4) * 8, ch = (lane >> 3) & 1;
 #pragma unroll
-          for (int h = 0; h < D / 64; ++h)
-            *reinterpret_cast<uint4*>(tile + h * (kPgTile * 128) +
-                                      (warp * 16 + valid + (i >> 3)) * 128 + (i & 7) * 16) =
-                make_uint4(0, 0, 0, 0);
-        __syncwarp();
-      }
-      // P is rounded to bf16 for the product (2^-9 of each weight); l is not.
-      const uint32_t b0 = transpose8x8(pack_bf16x2(pr[0], pr[1]));
-      const uint32_t b1 = transpose8x8(pack_bf16x2(pr[2], pr[3]));
-      const uint32_t base = smem_u32(tile) + warp * 16 * 128;
-      const int row = (lane & 7) + (lane >> 4) * 8, ch = (lane >> 3) & 1;
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const int chunk = mt * 2 + ch;
-        uint32_t a[4];
-        ldsm4_t(base + (chunk >> 3) * (kPgTile * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4),
-                a);
-        mma16816(acc[mt], a[0], a[1], a[2], a[3], b0, b1);
-      }
+    for (int mt = 0; mt < MT; ++mt) {
+      const int chunk = mt * 2 + ch;
+      uint32_t a[4];
+      ldsm4_t(base + (chunk >> 3) * (kPgTile * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4),
+              a);
+      mma16816(acc[mt], a[0], a[1], a[2], a[3], b0, b1);
     }
   };
 
   int n_skipped = 0;
-  uint32_t v_used = 0, v_par = 0;  // warp 0 lane 0: V slots in use, parity of their last copy
+  uint32_t v_used = 0, v_par = 0;  // warp 0: V slots in use, parity of their last copy
   if constexpr (!SKIP) {
     for (int t = 0; t < ntiles; ++t) {
       const int s = t % NS;
@@ -467,14 +432,11 @@ __global__ void __launch_bounds__(kPgThreads, PagedCfg<D, Q4>::kCtas)
     for (int t = 0; t < ntiles + kPgLag; ++t) {
       const bool live = t < ntiles;
       float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      int page[4];
+      int page = 0;
       if (live) {
         const int s = t % NS;
         mbar_wait(kfull(s), (t / NS) & 1, abort_flag);
-        if (tid == 0) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) page[i] = ids[s * 4 + i];
-        }
+        if (warp == 0) page = ids[s * 4 + ln.sub];
         scores(t, x);
         __syncwarp();
         if (lane == 0) mbar_arrive(kfree(s));
@@ -501,10 +463,13 @@ __global__ void __launch_bounds__(kPgThreads, PagedCfg<D, Q4>::kCtas)
         }
         keep = !__all_sync(0xffffffffu, pass);
         if (keep) {
-          if (tid == 0 && !*abort_flag) {
-            fetch(true, j0 + t, t % NS, page);
-            v_used |= 1u << (t % NS);
-            v_par ^= 1u << (t % NS);
+          if (warp == 0) {
+            const bool go = __all_sync(0xffffffffu, !*abort_flag);
+            fetch(1, go && lane < 8, j0 + t, t % NS, page);
+            if (go) {
+              v_used |= 1u << (t % NS);
+              v_par ^= 1u << (t % NS);
+            }
           }
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
@@ -542,18 +507,7 @@ __global__ void __launch_bounds__(kPgThreads, PagedCfg<D, Q4>::kCtas)
     }
   }
 
-  // ---- merge the warps' O^T, row sums and references; write the split.
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
-      if constexpr (Q4) {
-#pragma unroll
-        for (int gr = 0; gr < NG; ++gr)
-          zacc[gr][i] += __shfl_xor_sync(0xffffffffu, zacc[gr][i], o);
-      }
-    }
+  // ---- merge the warps; write the split.
   __syncthreads();  // with the producer: every warp is past its last use of the rings
   if (*abort_flag) {
     if (SKIP && tid == 0) {
@@ -563,50 +517,14 @@ __global__ void __launch_bounds__(kPgThreads, PagedCfg<D, Q4>::kCtas)
     }
     return;
   }
-  constexpr int RS = D + 4;  // row stride of the merge buffer: spreads the banks
-  float* red = reinterpret_cast<float*>(smem);
-  float2* stat = reinterpret_cast<float2*>(smem + C::kStat);
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int d = Q4 ? (mt >> 1) * 32 + 4 * g + 2 * (mt & 1) + (i >> 1) : mt * 16 + g + (i >> 1) * 8;
-      const int h = 2 * c + (i & 1);
-      red[(warp * 8 + h) * RS + d] = acc[mt][i] + (Q4 ? zacc[mt >> 1][i & 1] : 0.f);
-    }
-  if (g == 0) {
-    stat[warp * 8 + 2 * c] = make_float2(m[0], l[0]);
-    stat[warp * 8 + 2 * c + 1] = make_float2(m[1], l[1]);
-  }
-  named_bar_sync(1, kPgWarps * 32);
+  paged_merge_warps<D, kPgWarps>(p, reinterpret_cast<float*>(smem),
+                                 reinterpret_cast<float2*>(smem + C::kStat), head0, split, tid, m,
+                                 l, [&](int mt, int i) {
+                                   return PagedCell{mt * 16 + g + (i >> 1) * 8, acc[mt][i]};
+                                 });
   if (tid == 0 && p.counts) {
     atomicAdd(&p.counts[0], (unsigned long long)n_skipped);
     atomicAdd(&p.counts[1], (unsigned long long)ntiles);
-  }
-  for (int i = tid; i < p.G * D; i += kPgWarps * 32) {
-    const int h = i / D, d = i % D;
-    float2 st[kPgWarps];
-    float mx = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kPgWarps; ++w) {
-      st[w] = stat[w * 8 + h];
-      mx = fmaxf(mx, st[w].x);
-    }
-    float sum = 0.f, o = 0.f;
-#pragma unroll
-    for (int w = 0; w < kPgWarps; ++w) {
-      const float e = st[w].x == -INFINITY ? 0.f : ex2_approx(st[w].x - mx);
-      sum = fmaf(e, st[w].y, sum);
-      o = fmaf(e, red[(w * 8 + h) * RS + d], o);
-    }
-    const float lse = (mx + __log2f(sum)) * 0.69314718055994531f;
-    if (p.S == 1) {
-      p.o[(head0 + h) * D + d] = __float2bfloat16_rn(o / sum);
-      if (d == 0) p.lse[head0 + h] = lse;
-    } else {
-      p.o_part[((head0 + h) * p.S + split) * D + d] = o / sum;
-      if (d == 0) p.lse_part[(head0 + h) * p.S + split] = lse;
-    }
   }
 }
 

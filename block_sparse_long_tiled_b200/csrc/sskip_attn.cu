@@ -16,6 +16,7 @@
 #include <vector>
 
 #include "../../include/sskip_attn.h"
+#include "decode_paged4_sm100.cuh"
 #include "decode_paged_sm100.cuh"
 #include "decode_sm100.cuh"
 #include "kvcache_sm100.cuh"
@@ -830,25 +831,33 @@ bool make_page_map(CUtensorMap* map, const void* base, int d, long long rows, in
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool Q4, bool SKIP>
-int launch_decode_paged(const CUtensorMap& mk, const CUtensorMap& mv, const PagedDecodeParams& p,
-                        cudaStream_t st) {
-  auto kernel = decode_paged_kernel<D, Q4, SKIP>;
-  const int smem = PagedCfg<D, Q4>::kAlloc;
-  if (ensure_smem(reinterpret_cast<const void*>(kernel), smem) != cudaSuccess)
-    return SSKIP_ERR_CUDA;
-  kernel<<<dim3(p.S, p.Hkv, p.B), kPgThreads, smem, st>>>(mk, mv, p);
+template <int D>
+int launch_paged_combine(const PagedDecodeParams& p, cudaStream_t st) {
   if (cudaGetLastError() != cudaSuccess) return SSKIP_ERR_CUDA;
-  if (p.S == 1) return SSKIP_OK;
+  if (p.S == 1) return SSKIP_OK;  // the split kernel wrote the result
   decode_paged_combine_kernel<D><<<(unsigned)(p.B * p.Hq), 128, 0, st>>>(p);
   return cudaGetLastError() == cudaSuccess ? SSKIP_OK : SSKIP_ERR_CUDA;
 }
 
-template <int D, bool Q4>
+template <int D, bool SKIP>
 int launch_decode_paged(const CUtensorMap& mk, const CUtensorMap& mv, const PagedDecodeParams& p,
                         cudaStream_t st) {
-  return p.tsf > 0.f ? launch_decode_paged<D, Q4, true>(mk, mv, p, st)
-                     : launch_decode_paged<D, Q4, false>(mk, mv, p, st);
+  auto kernel = decode_paged_kernel<D, SKIP>;
+  const int smem = PagedCfg<D>::kAlloc;
+  if (ensure_smem(reinterpret_cast<const void*>(kernel), smem) != cudaSuccess)
+    return SSKIP_ERR_CUDA;
+  kernel<<<dim3(p.S, p.Hkv, p.B), kPgThreads, smem, st>>>(mk, mv, p);
+  return launch_paged_combine<D>(p, st);
+}
+
+template <int D, bool SKIP>
+int launch_decode_paged4(const PagedDecodeParams& p, cudaStream_t st) {
+  auto kernel = decode_paged4_kernel<D, SKIP>;
+  const int smem = Paged4Cfg<D, SKIP>::kTotal;
+  if (ensure_smem(reinterpret_cast<const void*>(kernel), smem) != cudaSuccess)
+    return SSKIP_ERR_CUDA;
+  kernel<<<dim3(p.S, p.Hkv, p.B), kP4Threads, smem, st>>>(p);
+  return launch_paged_combine<D>(p, st);
 }
 
 }  // namespace
@@ -1083,21 +1092,24 @@ SSKIP_API int sskip_attn_decode_paged(const void* q, const void* k_pages, const 
   p.n_k_max = (int)(((long long)max_pages * page_size + kPgTile - 1) / kPgTile);
   p.scale_log2 = (float)((double)sm_scale * 1.4426950408889634);
   p.tsf = threshold_scale_factor;
-  CUtensorMap mk{}, mv{};
-  if (kv_format == SSKIP_KV_BF16) {
-    const long long n = (long long)num_pages * Hkv * page_size;
-    const int box = std::min(page_size, kPgTile);
-    if (!make_page_map(&mk, k_pages, d, n, box) || !make_page_map(&mv, v_pages, d, n, box))
-      return SSKIP_ERR_CUDA;
-  }
   if (skip_count && cudaMemsetAsync(skip_count, 0, 2 * sizeof(unsigned long long), st) != cudaSuccess)
     return SSKIP_ERR_CUDA;
   if (tile_state &&
       cudaMemsetAsync(tile_state, 0, (size_t)B * Hkv * p.n_k_max, st) != cudaSuccess)
     return SSKIP_ERR_CUDA;
-  if (kv_format == SSKIP_KV_INT4)
-    return d == 128 ? launch_decode_paged<128, true>(mk, mv, p, st)
-                    : launch_decode_paged<64, true>(mk, mv, p, st);
-  return d == 128 ? launch_decode_paged<128, false>(mk, mv, p, st)
-                  : launch_decode_paged<64, false>(mk, mv, p, st);
+  const bool skip = threshold_scale_factor > 0.f;
+  if (kv_format == SSKIP_KV_INT4) {
+    if (d == 128) return skip ? launch_decode_paged4<128, true>(p, st)
+                              : launch_decode_paged4<128, false>(p, st);
+    return skip ? launch_decode_paged4<64, true>(p, st) : launch_decode_paged4<64, false>(p, st);
+  }
+  CUtensorMap mk, mv;
+  const long long n = (long long)num_pages * Hkv * page_size;
+  const int box = std::min(page_size, kPgTile);
+  if (!make_page_map(&mk, k_pages, d, n, box) || !make_page_map(&mv, v_pages, d, n, box))
+    return SSKIP_ERR_CUDA;
+  if (d == 128) return skip ? launch_decode_paged<128, true>(mk, mv, p, st)
+                            : launch_decode_paged<128, false>(mk, mv, p, st);
+  return skip ? launch_decode_paged<64, true>(mk, mv, p, st)
+              : launch_decode_paged<64, false>(mk, mv, p, st);
 }
