@@ -1,19 +1,36 @@
 // decode_paged4_sm100.cuh -- the split-KV Skip-Softmax decode over 4-bit pages.
 //
 // The rule, the grid and the products are those of the bf16 kernel
-// (decode_paged_sm100.cuh); what differs is what bounds it.  A tile is a
-// quarter of the bytes, so the instructions that widen the codes decide: a
-// consumer warp therefore owns WHOLE tiles (tile t belongs to warp t mod 4),
-// which spreads everything that is not widening -- waits, the reference check,
-// the vote -- over 64 keys instead of 16.
+// (decode_paged_sm100.cuh); what differs is what bounds it.  A tile is 0.31 of
+// the bytes, so the instructions that widen the codes decide, and the kernel is
+// laid out to spend few others and to keep many warps at it: there is no
+// producer, every warp fetches its own tiles into slots that only it uses, and
+// a warp owns WHOLE units of keys (32 without a threshold, a 64-key tile with
+// one), so that waits, reference checks and votes spread over all of them.
 //
-// Keys: S = sum over groups of sc (q . (n - 8)) + (8 sc + mn) sum(q).  The codes
-// enter the tensor cores as the exact bf16 integers n - 8; a group's scale
-// multiplies its 32-term product in fp32; the last term is one more product,
-// of the record's own (sc, mn) pairs with (8 sum q, sum q) split into three
-// bf16 parts that together hold its 24 bits.
-// Values: the group's scale joins P before the rounding to bf16, the part that
-// does not depend on the code, P (8 sc + mn), is summed in fp32.
+// Codes.  A bf16 whose sign and upper seven exponent bits are 0 is its low byte
+// times 2^-133: the subnormals and the first binade are evenly spaced.  So a
+// mask alone turns two nibbles of a word into the bf16 operands n 2^-133 and
+// 16 n 2^-133, and a shift by 8 and two masks do the other two: five
+// instructions for eight codes, exactly, with no bias to take off.  Q and P
+// carry 2^48 each, which keeps every product and sum a normal fp32 number
+// (2^-85 times what it stands for), and the 16 goes into Q (or, for the
+// values, into the result's rows).  Measured clocks of a sub-partition for one
+// instruction of a warp: logic, shifts, packed bf16 arithmetic 2, the 8x8
+// transpose 4, m16n8k16 bf16 8, m16n8k32 e4m3 24.  The logic pipe is the
+// fullest.  64 sequences of 16K-32K (8 kv heads, d = 128, no threshold), other
+// things equal: 583 us with e4m3 operands, 504 with the codes as 128 + n and a
+// subtraction, 473 with these; 450 with full and last records apart.
+//
+// Keys: S = sum over groups of sc (q . n) + mn sum(q).  A group's scale multiplies
+// its 32-term product in fp32; the last term is one more product, of the
+// record's own (sc, mn) pairs with (0, sum q) in three bf16 parts that hold its
+// 24 bits.
+//
+// Values: O = sum of P' (n - 8) + P (8 sc + mn) with P' = P sc, the group's scale
+// joining P before its rounding to bf16.  The -8 (it halves what that rounding
+// costs) is one more product for each group, of the number 8 with the same
+// rounded P'; the part that does not depend on the code is summed in fp32.
 //
 // With a threshold the warps take one decision for four tiles at a time: each
 // publishes its tile's maxima, and after one named barrier all walk the four
@@ -21,46 +38,57 @@
 // tile, which is fetched after the decision and used one round later.
 #pragma once
 
+#include <type_traits>
+
 #include "decode_paged_sm100.cuh"
 
 namespace sskip {
 
-constexpr int kP4Warps = 4;                      // consumer warps
-constexpr int kP4Threads = (kP4Warps + 1) * 32;
+constexpr int kP4Warps = 4;
+constexpr int kP4Threads = kP4Warps * 32;
 
 template <int D, bool SKIP>
 struct Paged4Cfg {
-  static constexpr int kTileBytes = 4 * Kv4<D>::kRecord;
-  static constexpr int kNK = 2 * kP4Warps;           // ring slots of K
-  static constexpr int kNV = 2 * kP4Warps;
-  static constexpr int kCtas = 2;                    // per SM
-  static constexpr int kK = 0;
-  static constexpr int kV = kK + kNK * kTileBytes;
-  static constexpr int kS = kV + kNV * kTileBytes;  // [W][2][64][8] fp32 scores
+  static constexpr int kUnit = SKIP ? kPgTile : 32;        // keys a warp takes at a time
+  static constexpr int kBytes = kUnit / 16 * Kv4<D>::kRecord;
+  static constexpr int kSlots = SKIP ? 1 : 3;              // K and V slots of a warp
+  static constexpr int kCtas = 3;                          // per SM
+  static constexpr int kBars = SKIP ? 2 : kSlots;          // of a warp: K and V, or the slots
+  static constexpr int kK = 0;                              // [W][slots]
+  static constexpr int kV = kK + kP4Warps * kSlots * kBytes;
+  static constexpr int kS = kV + kP4Warps * kSlots * kBytes;  // [W][2][64][8] fp32 scores
   static constexpr int kMax = kS + (SKIP ? kP4Warps * 2 * kPgTile * 8 * 4 : 0);  // [2][8][W]
-  static constexpr int kStat = kMax + 2 * 8 * kP4Warps * 4;    // [W][8] (m, l)
-  static constexpr int kIds = kStat + kP4Warps * 8 * 8;        // [NK][4] pages of a tile
-  static constexpr int kBar = kIds + kNK * 16;
-  static constexpr int kTotal = kBar + 2 * (kNK + kNV) * 8 + 16;
-  static_assert(kP4Warps * 8 * (D + 4) * 4 <= kS, "the merge of the warps fits the rings");
-  // Every slot belongs to one warp: only then does that warp wait for the
-  // slot's phases one after the other, and no parity can be an older phase's.
-  static_assert(kNK % kP4Warps == 0 && kNV % kP4Warps == 0, "a slot's tiles belong to one warp");
+  static constexpr int kMerge = kP4Warps * 8 * (D + 4) * 4;   // reuses the slots and the scores
+  static constexpr int kStat = (kMax > kMerge ? kMax : kMerge) + 2 * 8 * kP4Warps * 4;
+  static constexpr int kBar = kStat + kP4Warps * 8 * 8;
+  static constexpr int kTotal = kBar + kP4Warps * kBars * 8 + 16;
 };
 
-// The four pairs of a 4-bit word as bf16 pairs n - 8: the code under the
-// exponent of 128 is 128 + n, and taking 136 away is exact.
+constexpr uint32_t kEights = 0x00080008u;              // a pair of 8s, in units of 2^-133
+constexpr float kP4Up = 281474976710656.f;            // 2^48: on Q and P
+constexpr float kP4Log = 48.f;
+constexpr float kP4Unit = 2.5849394142282115e-26f;     // 2^-85: what a product stands for
+constexpr float kP4PerUnit = 3.8685626227668134e25f;   // 2^85
+
+// The four pairs of a 4-bit word as bf16 pairs, n 2^-133 (even) and
+// 16 n 2^-133 (odd nibbles).
 __device__ __forceinline__ void widen_codes(uint32_t w, uint32_t (&r)[4]) {
-  const __nv_bfloat162 bias = __halves2bfloat162(__ushort_as_bfloat16(0x4308),
-                                                 __ushort_as_bfloat16(0x4308));
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t x = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-    const __nv_bfloat162 y = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), bias);
-    r[i] = *reinterpret_cast<const uint32_t*>(&y);
-  }
+  const uint32_t v = w >> 8;
+  r[0] = w & 0x000F000Fu;
+  r[1] = w & 0x00F000F0u;
+  r[2] = v & 0x000F000Fu;
+  r[3] = v & 0x00F000F0u;
 }
 
+// D = A B, without an accumulator to clear first.
+__device__ __forceinline__ void mma16816_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 // N words of shared memory, aligned to N * 4 bytes (N = 2 or 4).
 template <int N>
 __device__ __forceinline__ void lds_words(uint32_t (&w)[N], const uint8_t* p) {
@@ -77,7 +105,7 @@ template <int D, bool SKIP>
 __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
     decode_paged4_kernel(const PagedDecodeParams p) {
   using C = Paged4Cfg<D, SKIP>;
-  constexpr int NK = C::kNK, NV = C::kNV, W = kP4Warps;
+  constexpr int W = kP4Warps, UNIT = C::kUnit, NREC = UNIT / 16;
   constexpr int NG = D / 32;   // groups of a row
   constexpr int MT = D / 16;   // 16-row tiles of O^T
   constexpr int REC = Kv4<D>::kRecord, CODES = Kv4<D>::kCodes;
@@ -101,126 +129,140 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
     paged_empty_split<D>(p, head0, split, tid, kP4Threads);
     return;
   }
+  const int key0 = j0 * kPgTile;                              // of the split
+  const int keys = min(Lb, (j0 + ntiles) * kPgTile) - key0;
+  const int units = (keys + UNIT - 1) / UNIT;
 
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBar);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kBar + 2 * (NK + NV) * 8);
-  int* ids = reinterpret_cast<int*>(smem + C::kIds);
-  const uint32_t k_smem = smem_u32(smem + C::kK), v_smem = smem_u32(smem + C::kV);
-  auto kfull = [&](int s) { return smem_u32(&bars[s]); };
-  auto kfree = [&](int s) { return smem_u32(&bars[NK + s]); };
-  auto vfull = [&](int s) { return smem_u32(&bars[2 * NK + s]); };
-  auto vfree = [&](int s) { return smem_u32(&bars[2 * NK + NV + s]); };
-  if (tid == 0) {
-    for (int s = 0; s < 2 * (NK + NV); ++s) mbar_init(smem_u32(&bars[s]), 1);
-    *abort_flag = 0;
+  const uint32_t bars = smem_u32(smem + C::kBar) + warp * C::kBars * 8;  // this warp's
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kBar + W * C::kBars * 8);
+  uint8_t* kbuf = smem + C::kK + warp * C::kSlots * C::kBytes;
+  uint8_t* vbuf = smem + C::kV + warp * C::kSlots * C::kBytes;
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < C::kBars; ++i) mbar_init(bars + i * 8, 1);
+    if (warp == 0) *abort_flag = 0;
     fence_mbar_init();
   }
   __syncthreads();
 
-  // A whole warp: tile j's copies of K (val = 0) or V into ring slot s; each
-  // lane brings the page of its copy.
-  const PagedLane ln(p.c, lane);
-  const uint32_t copy_bytes = (uint32_t)(ln.rows >> 4) * REC;
-  auto fetch = [&](int val, bool on, int j, int s, int page) {
-    const uint32_t bar = val ? vfull(s) : kfull(s);
-    const uint32_t dst = (val ? v_smem : k_smem) + s * C::kTileBytes;
-    const int n = ln.copies(j, Lb);
-    const bool ok = dev_check(j < n_k && n >= 1 && n <= 4 && s < (val ? NV : NK));
-    if (on && ln.sub == 0 && ln.half == 0) {
-      if (ok) mbar_arrive_expect_tx(bar, n * copy_bytes);
+  // ---- the copies of a unit: one when a page holds it, else UNIT / P, of which
+  // those behind the last key are not fetched.  Every copy is one lane's (lanes
+  // 0 .. 3 K, lanes 4 .. 7 V), which follows its own first key through the split
+  // and looks a copy's page up well before it issues the copy.
+  const int* table = p.c.block_table + (size_t)b * p.c.max_pages;
+  const int shift = p.c.page_shift, row_shift = min(shift, SKIP ? 6 : 5), rows = 1 << row_shift;
+  const int sub = lane & 3, end = key0 + keys;
+  const uint32_t copy_bytes = (uint32_t)(rows >> 4) * REC;
+  const bool copies = lane < 8 && sub < (UNIT >> row_shift);
+  const uint8_t* pool = ((lane & 4) ? p.c.v_pages : p.c.k_pages) +
+                        ((size_t)kvh << shift) * (REC / 16);
+  const uint32_t page_bytes = (uint32_t)(p.Hkv << shift) * (REC / 16);
+  const uint32_t dst = smem_u32((lane & 4) ? vbuf : kbuf) + sub * copy_bytes;
+  auto page_at = [&](int key) {  // key: this lane's first key of a unit
+    int page = copies && key < end ? __ldg(table + (key >> shift)) : 0;
+    if ((uint32_t)page >= (uint32_t)p.c.num_pages) {
+      latch_status(kStatusInvalidArg);  // read as page 0
+      page = 0;
+    }
+    return page;
+  };
+  // The unit whose first key (of lane sub = 0) is k0, this lane's being `key`.
+  // which: bit 0 K, bit 1 V.  Called by the whole warp, on a slot whose last
+  // copies have arrived.
+  auto fetch = [&](int k0, int key, int page, int which, int slot, uint32_t bar) {
+    const bool ok = dev_check(k0 < end && slot < C::kSlots);
+    if (lane == 0) {
+      const uint32_t n = (uint32_t)min(UNIT, (end - k0 + rows - 1) >> row_shift << row_shift);
+      if (ok) mbar_arrive_expect_tx(bar, (n >> 4) * REC * (which == 3 ? 2 : 1));
       else mbar_arrive(bar);  // the phase completes without data
     }
     __syncwarp();
-    if (on && ok && ln.sub < n && ln.half == 0)
-      bulk_load(dst + ln.sub * copy_bytes,
-                (val ? p.c.v_pages : p.c.k_pages) + ln.row(j, page, p.Hkv, kvh) * (REC / 16),
+    if (ok && copies && key < end && ((which >> (lane >> 2)) & 1))
+      bulk_load(dst + slot * C::kBytes,
+                pool + (size_t)page * page_bytes +
+                    (uint32_t)(key & ((1 << shift) - 1)) * (uint32_t)(REC / 16),
                 copy_bytes, bar);
   };
+  // A wait that gives up is the same for the whole warp; what it waited for
+  // stays in flight and its slot is not fetched into again.
+  auto await = [&](uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+  };
 
-  if (warp == W) {
-    // ------------------------------------------------------------ producer
-    const int* table = p.c.block_table + (size_t)b * p.c.max_pages;
-    const int val = SKIP ? 0 : ln.val;
-    const bool mine = lane < (SKIP ? 8 : 16) && ln.half == 0;
-    // The page of this lane's copy of a tile, loaded a tile ahead.
-    auto page_of = [&](int j) {
-      return mine && j < n_k && ln.sub < ln.copies(j, Lb) ? __ldg(table + ln.slot(j)) : 0;
-    };
-    static_assert(SKIP || NK == NV, "one slot counter for both rings");
-    int issued = 0, s = 0, par = 1, next = page_of(j0);
-    bool ok = true;
-    for (int t = 0; t < ntiles; ++t) {
-      const int j = j0 + t, page = paged_checked(p.c, next);
-      next = page_of(j + 1);
-      if (t >= NK) ok = mbar_wait(val ? vfree(s) : kfree(s), par, abort_flag);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      if (SKIP && mine) ids[s * 4 + ln.sub] = page;
-      __syncwarp();
-      fetch(val, mine, j, s, page);
-      issued = t + 1;
-      if (++s == NK) { s = 0; par ^= 1; }
+  int u = warp;  // this warp's next unit to compute
+  constexpr int STEP = W * UNIT;
+  int key = key0 + u * UNIT + sub * rows;  // this lane's first key of the next unit to fetch
+  int page = page_at(key);
+  int next_page = 0;       // SKIP: of the unit after the one `page` belongs to
+  bool k_inflight = false; // SKIP
+  if (SKIP) {
+    if (u < units) {
+      fetch(key0 + u * UNIT, key, page, 1, 0, bars);
+      k_inflight = true;
     }
-    __syncthreads();
-    if (*abort_flag && lane == 0) {  // wait out the copies in flight before the CTA exits
-      int no_abort = 0;
-      for (int i = 0; i < NK; ++i)
-        if (issued > i) {
-          mbar_wait(kfull(i), ((issued - 1 - i) / NK) & 1, &no_abort);
-          if (!SKIP) mbar_wait(vfull(i), ((issued - 1 - i) / NK) & 1, &no_abort);
-        }
-    }
-    return;
+    next_page = page_at(key + STEP);
+  } else {
+#pragma unroll
+    for (int i = 0; i < C::kSlots; ++i)
+      if (u + i * W < units) {
+        fetch(key0 + (u + i * W) * UNIT, key, page, 3, i, bars + i * 8);
+        key += STEP;
+        page = page_at(key);
+      }
   }
 
-  // -------------------------------------------------------------- consumers
+  // ---- Q^T of head g: the d's that the key words hold at this lane, times 2^48
+  // (even nibbles) or 2^44 (odd ones): a power of two, so still exact.
   const int g = lane >> 2, c = lane & 3;
-  // Q^T fragments of head g: the d's that the key words hold at this lane.
   uint32_t qf[MT][2];
-  uint32_t zf[3] = {0u, 0u, 0u};  // (8 sum q, sum q) of group c, in three bf16 parts
+  uint32_t zf[3] = {0u, 0u, 0u};  // (0, sum q) of group c, in three bf16 parts
   {
     const __nv_bfloat16* q = p.q + (head0 + g) * D;
-#pragma unroll
-    for (int kt = 0; kt < MT; ++kt)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int d = (kt >> 1) * 32 + 8 * c + 2 * ((kt & 1) * 2 + i);
-        qf[kt][i] = g < p.G ? *reinterpret_cast<const uint32_t*>(q + d) : 0u;
-      }
     float mine = 0.f;
 #pragma unroll
     for (int gr = 0; gr < NG; ++gr) {
-      float s = 0.f;
+      float x[8], s = 0.f;
+      uint4 w = make_uint4(0u, 0u, 0u, 0u);
+      if (g < p.G) w = *reinterpret_cast<const uint4*>(q + gr * 32 + c * 8);
+      bf16x8_to_f32(w, x);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t w = qf[2 * gr + (i >> 1)][i & 1];
-        s += __uint_as_float(w << 16) + __uint_as_float(w & 0xFFFF0000u);
+        const float up = (i & 1) ? kP4Up / 16.f : kP4Up;
+        qf[2 * gr + (i >> 1)][i & 1] = pack_bf16x2(x[2 * i] * up, x[2 * i + 1] * up);
+        s += x[2 * i] + x[2 * i + 1];
       }
       s += __shfl_xor_sync(0xffffffffu, s, 1);
       s += __shfl_xor_sync(0xffffffffu, s, 2);
-      if (c == gr) mine = s;
+      if (c == gr) mine = s * kP4Unit;
     }
-    float x = 8.f * mine, y = mine;
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
-      zf[i] = pack_bf16x2(x, y);
-      x -= __uint_as_float(zf[i] << 16);
-      y -= __uint_as_float(zf[i] & 0xFFFF0000u);
+      zf[i] = pack_bf16x2(0.f, mine);
+      mine -= __uint_as_float(zf[i] & 0xFFFF0000u);
     }
   }
+  const float sl = p.scale_log2 * kP4PerUnit;
   const float log2_t = SKIP ? (float)log2((double)p.tsf / (double)Lb) : -INFINITY;
-  const float sl = p.scale_log2;
 
-  float acc[MT][4];    // O^T
-  float zacc[NG][2];   // sum of p (8 sc + mn)
-  float l[2] = {0.f, 0.f};  // heads 2 c, 2 c + 1
+  float acc[MT][4];                // O^T of the codes, in units of 2^-133
+  float eight[NG][4];              // 8 sum of P', in the same units, the same in every row
+  float zacc[NG][2];               // sum of p (8 sc + mn)
+  float l[2] = {0.f, 0.f};         // heads 2 c, 2 c + 1
 #pragma unroll
   for (int i = 0; i < MT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
 #pragma unroll
-  for (int i = 0; i < NG; ++i) zacc[i][0] = zacc[i][1] = 0.f;
+  for (int i = 0; i < NG; ++i) {
+    zacc[i][0] = zacc[i][1] = 0.f;
+    eight[i][0] = eight[i][1] = eight[i][2] = eight[i][3] = 0.f;
+  }
 
-  // Logits (before sm_scale) of a record's 16 keys: x[0..1] key g, x[2..3] key
+  // A record is worked on as a full one or (tail) as one with `valid` < 16 keys.
+  constexpr std::false_type full;
+  constexpr std::true_type part;
+
+  // Logits (before sm_scale, times 2^-85) of a record's 16 keys: x[0..1] key g, x[2..3] key
   // g + 8, heads 2 c and 2 c + 1; the keys from `valid` on -> -inf.
-  auto scores = [&](const uint8_t* rec, int valid, float (&x)[4]) {
+  auto scores = [&](auto tail, const uint8_t* rec, int valid, float (&x)[4]) {
     uint32_t wa[NG], wb[NG], pa[NG], pb[NG];
     lds_words<NG>(wa, rec + g * (D / 2) + c * NG * 4);
     lds_words<NG>(wb, rec + (g + 8) * (D / 2) + c * NG * 4);
@@ -228,16 +270,15 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
     lds_words<NG>(pb, rec + CODES + (g + 8) * NG * 4);
     const uint32_t z0 = *reinterpret_cast<const uint32_t*>(rec + CODES + (g * NG + (c % NG)) * 4);
     const uint32_t z1 = *reinterpret_cast<const uint32_t*>(rec + CODES + ((g + 8) * NG + (c % NG)) * 4);
-    x[0] = x[1] = x[2] = x[3] = 0.f;
-    mma16816(x, z0, z1, z0, z1, zf[0], zf[1]);
+    mma16816_zero(x, z0, z1, z0, z1, zf[0], zf[1]);
     mma16816(x, z0, z1, z0, z1, zf[2], 0u);
 #pragma unroll
     for (int gr = 0; gr < NG; ++gr) {
       uint32_t a[4], e[4];
       widen_codes(wa[gr], a);
       widen_codes(wb[gr], e);
-      float y[4] = {0.f, 0.f, 0.f, 0.f};
-      mma16816(y, a[0], e[0], a[1], e[1], qf[2 * gr][0], qf[2 * gr][1]);
+      float y[4];
+      mma16816_zero(y, a[0], e[0], a[1], e[1], qf[2 * gr][0], qf[2 * gr][1]);
       mma16816(y, a[2], e[2], a[3], e[3], qf[2 * gr + 1][0], qf[2 * gr + 1][1]);
       const float sa = __uint_as_float(pa[gr] << 16), sb = __uint_as_float(pb[gr] << 16);
       x[0] = fmaf(sa, y[0], x[0]);
@@ -245,7 +286,7 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
       x[2] = fmaf(sb, y[2], x[2]);
       x[3] = fmaf(sb, y[3], x[3]);
     }
-    if (valid < 16) {
+    if constexpr (tail.value) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (g + (i >> 1) * 8 >= valid) x[i] = -INFINITY;
@@ -253,21 +294,20 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
   };
 
   // O^T += V^T P^T over a record's 16 keys.
-  auto accumulate = [&](const uint8_t* rec, int valid, const float (&pr)[4]) {
+  auto accumulate = [&](auto tail, uint8_t* rec, int valid, const float (&pr)[4]) {
+    if constexpr (tail.value) {
+      // Behind the last key the record holds what an earlier sequence left:
+      // its codes are numbers, its scales need not be.  The slot is not
+      // fetched into again: this is the sequence's last record.
+      for (int i = valid * NG + lane; i < 16 * NG; i += 32)
+        reinterpret_cast<uint32_t*>(rec + CODES)[i] = 0u;
+      __syncwarp();
+    }
     uint32_t w0[NG], w1[NG], pa[NG], pb[NG];
     lds_words<NG>(w0, rec + lane * NG * 4);
     lds_words<NG>(w1, rec + (32 + lane) * NG * 4);
     lds_words<NG>(pa, rec + CODES + g * NG * 4);
     lds_words<NG>(pb, rec + CODES + (g + 8) * NG * 4);
-    if (valid < 16) {
-      // Behind the last key the record holds what an earlier sequence left:
-      // its codes are numbers, its scales need not be.
-#pragma unroll
-      for (int gr = 0; gr < NG; ++gr) {
-        if (g >= valid) pa[gr] = 0u;
-        if (g + 8 >= valid) pb[gr] = 0u;
-      }
-    }
 #pragma unroll
     for (int gr = 0; gr < NG; ++gr) {
       const float sa = __uint_as_float(pa[gr] << 16), sb = __uint_as_float(pb[gr] << 16);
@@ -283,6 +323,7 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
       widen_codes(w1[gr], e);
       mma16816(acc[2 * gr], a[0], a[1], e[0], e[1], b0, b1);
       mma16816(acc[2 * gr + 1], a[2], a[3], e[2], e[3], b0, b1);
+      mma16816(eight[gr], kEights, kEights, kEights, kEights, b0, b1);
     }
   };
 
@@ -293,7 +334,10 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
         acc[i][0] *= a0; acc[i][1] *= a1; acc[i][2] *= a0; acc[i][3] *= a1;
       }
 #pragma unroll
-      for (int i = 0; i < NG; ++i) { zacc[i][0] *= a0; zacc[i][1] *= a1; }
+      for (int i = 0; i < NG; ++i) {
+        zacc[i][0] *= a0; zacc[i][1] *= a1;
+        eight[i][0] *= a0; eight[i][1] *= a1; eight[i][2] *= a0; eight[i][3] *= a1;
+      }
       l[0] *= a0;
       l[1] *= a1;
     }
@@ -301,90 +345,111 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
 
   float m[2] = {-INFINITY, -INFINITY};  // reference of heads 2 c, 2 c + 1, in log2 units
   int n_skipped = 0;
-  // SKIP: this warp's two V slots: fetched into (and the parity of the last
-  // copy), and the phase to wait for next.
-  uint32_t v_used = 0, v_par = 0, v_phase = 0;
   if constexpr (!SKIP) {
     float mm[2] = {0.f, 0.f};  // m, or 0 while it is -inf
-    int ks = warp, kp = 0, vs = warp, vp = 0;
-    for (int t = warp; t < ntiles; t += W) {
-      mbar_wait(kfull(ks), kp, abort_flag);
-      mbar_wait(vfull(vs), vp, abort_flag);
-      const int left = Lb - (j0 + t) * kPgTile;
-      const uint8_t* krec = smem + C::kK + ks * C::kTileBytes;
-      const uint8_t* vrec = smem + C::kV + vs * C::kTileBytes;
+    auto record = [&](auto tail, uint8_t* krec, uint8_t* vrec, int valid) {
+      float x[4];
+      scores(tail, krec, valid, x);
+      // The reference moves only when a score is 2^8 above it: P stays below
+      // 2^8 (times 2^48) and most records need no exchange between the lanes.
+      float top[2] = {fmaxf(x[0], x[2]) * sl, fmaxf(x[1], x[3]) * sl};
+      if (__any_sync(0xffffffffu, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f)) {
+        float a[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1)
+            top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], o));
+          const float mn = fmaxf(m[h], top[h]);
+          a[h] = m[h] == mn ? 1.f : (m[h] == -INFINITY ? 0.f : ex2_approx(m[h] - mn));
+          m[h] = mn;
+          mm[h] = mn == -INFINITY ? 0.f : mn;
+        }
+        rescale(a[0], a[1]);
+      }
+      float pr[4];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) pr[h] = ex2_approx(fmaf(x[h], sl, kP4Log - mm[h & 1]));
+      l[0] += pr[0] + pr[2];
+      l[1] += pr[1] + pr[3];
+      accumulate(tail, vrec, valid, pr);
+    };
+    int slot = 0, done = 0;
+    uint32_t parity = 0;
+    for (; u < units; u += W, ++done) {
+      if (!await(bars + slot * 8, parity)) break;
+      uint8_t* krec = kbuf + slot * C::kBytes;
+      uint8_t* vrec = vbuf + slot * C::kBytes;
+      const int left = keys - u * UNIT;
+      if (left >= UNIT) {
 #pragma unroll 1
-      for (int i = 0; i < 4 && i * 16 < left; ++i) {
-        float x[4];
-        scores(krec + i * REC, left - i * 16, x);
-        // The reference moves only when a score is 2^8 above it: P stays
-        // below 2^8 and most records need no exchange between the lanes.
-        float top[2] = {fmaxf(x[0], x[2]) * sl, fmaxf(x[1], x[3]) * sl};
-        if (__any_sync(0xffffffffu, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f)) {
-          float a[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1)
-              top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], o));
-            const float mn = fmaxf(m[h], top[h]);
-            a[h] = (m[h] == -INFINITY) ? 0.f : ex2_approx(m[h] - mn);
-            m[h] = mn;
-            mm[h] = mn == -INFINITY ? 0.f : mn;
-          }
-          rescale(a[0], a[1]);
-        }
-        float pr[4];
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          pr[h] = ex2_approx(fmaf(x[h], sl, -mm[h & 1]));
-          l[h & 1] += pr[h];
-        }
-        accumulate(vrec + i * REC, left - i * 16, pr);
+        for (int i = 0; i < NREC; ++i) record(full, krec + i * REC, vrec + i * REC, 16);
+      } else {
+#pragma unroll 1
+        for (int i = 0; i * 16 < left; ++i) record(part, krec + i * REC, vrec + i * REC, left - i * 16);
       }
       if (p.tile_state && lane == 0)
-        p.tile_state[((size_t)b * p.Hkv + kvh) * p.n_k_max + j0 + t] = 1;
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(kfree(ks));
-        mbar_arrive(vfree(vs));
+        p.tile_state[((size_t)b * p.Hkv + kvh) * p.n_k_max + j0 + u * UNIT / kPgTile] = 1;
+      __syncwarp();  // every lane is past its reads of the slot
+      if (u + C::kSlots * W < units) {
+        fetch(key0 + (u + C::kSlots * W) * UNIT, key, page, 3, slot, bars + slot * 8);
+        key += STEP;
+        page = page_at(key);
       }
-      ks += W; if (ks >= NK) { ks -= NK; kp ^= 1; }
-      vs += W; if (vs >= NV) { vs -= NV; vp ^= 1; }
+      if (++slot == C::kSlots) { slot = 0; parity ^= 1; }
+    }
+    if (u < units) {  // gave up: wait out this warp's copies before the CTA exits
+      int no_abort = 0;
+      const int issued = min(done + C::kSlots, done + (units - u + W - 1) / W);
+      for (int i = done; i < issued; ++i)
+        mbar_wait(bars + (i % C::kSlots) * 8, (i / C::kSlots) & 1, &no_abort);
     }
   } else {
     float* wmax = reinterpret_cast<float*>(smem + C::kMax);
-    float* sbuf = reinterpret_cast<float*>(smem + C::kS) + warp * 2 * kPgTile * 8;
+    constexpr int SB = kPgTile * 8;  // a tile's scores: 64 keys, 8 heads
+    float* sbuf = reinterpret_cast<float*>(smem + C::kS) + warp * 2 * SB;
     float m_prev[2] = {0.f, 0.f}, a_prev[2] = {1.f, 1.f};  // of the round before
-    bool kept_prev = false;
+    bool kept_prev = false, v_inflight = false;
+    uint32_t k_count = 0, v_parity = 0;  // K tiles waited for; phase of V's next wait
+    int vkey = 0;  // this lane's first key of the round's tile
     const int rounds = (ntiles + W - 1) / W;
-    int ks = warp, kp = 0;
-    for (int r = 0; r <= rounds; ++r) {
-      const int t = r * W + warp;
-      const bool live = t < ntiles;
+    for (int r = 0; r <= rounds; ++r, u += W) {
+      const bool live = u < units;
       bool keep = false;
       float a[2] = {1.f, 1.f}, mm[2] = {0.f, 0.f};
+      int vpage = 0;
       if (r < rounds) {
-        int page = 0;
         if (live) {
-          mbar_wait(kfull(ks), kp, abort_flag);
-          page = ids[ks * 4 + ln.sub];
-          const int left = Lb - (j0 + t) * kPgTile;
-          const uint8_t* krec = smem + C::kK + ks * C::kTileBytes;
-          float* sb = sbuf + (r & 1) * kPgTile * 8;
+          const bool there = k_inflight && await(bars, k_count & 1);
+          if (there) { k_inflight = false; ++k_count; }
+          const int left = keys - u * UNIT;
+          float* sb = sbuf + (r & 1) * SB + g * 8 + 2 * c;
           float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll 1
-          for (int i = 0; i < 4 && i * 16 < left; ++i) {
+          auto record = [&](auto tail, int i) {
             float x[4];
-            scores(krec + i * REC, left - i * 16, x);
-            *reinterpret_cast<float2*>(sb + (i * 16 + g) * 8 + 2 * c) = make_float2(x[0], x[1]);
-            *reinterpret_cast<float2*>(sb + (i * 16 + g + 8) * 8 + 2 * c) = make_float2(x[2], x[3]);
+            scores(tail, kbuf + i * REC, left - i * 16, x);
+            *reinterpret_cast<float2*>(sb + i * 128) = make_float2(x[0], x[1]);
+            *reinterpret_cast<float2*>(sb + i * 128 + 64) = make_float2(x[2], x[3]);
             top[0] = fmaxf(top[0], fmaxf(x[0], x[2]));
             top[1] = fmaxf(top[1], fmaxf(x[1], x[3]));
+          };
+          if (left >= UNIT) {
+#pragma unroll 1
+            for (int i = 0; i < NREC; ++i) record(full, i);
+          } else {
+#pragma unroll 1
+            for (int i = 0; i * 16 < left; ++i) record(part, i);
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(kfree(ks));
-          ks += W; if (ks >= NK) { ks -= NK; kp ^= 1; }
+          __syncwarp();  // every lane is past its reads of the slot
+          vpage = page;
+          vkey = key;
+          if (u + W < units && there) {
+            key += STEP;
+            page = next_page;
+            fetch(key0 + (u + W) * UNIT, key, page, 1, 0, bars);
+            k_inflight = true;
+            next_page = page_at(key + STEP);
+          }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -421,71 +486,79 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
           mm[h] = m[h] == -INFINITY ? 0.f : m[h];
         }
         if (live) {
-          if (keep) {
-            const bool go = __all_sync(0xffffffffu, !*abort_flag);
-            fetch(1, go && lane < 8, j0 + t, (r & 1) * W + warp, page);
-            if (go) {
-              v_used |= 1u << (r & 1);
-              v_par ^= 1u << (r & 1);
-            }
-          } else {
-            n_skipped += 1;
-          }
+          if (!keep) n_skipped += 1;
           if (p.tile_state && lane == 0)
-            p.tile_state[((size_t)b * p.Hkv + kvh) * p.n_k_max + j0 + t] = keep ? 1 : 2;
+            p.tile_state[((size_t)b * p.Hkv + kvh) * p.n_k_max + j0 + u] = keep ? 1 : 2;
         }
       }
-      if (r > 0) {  // round r - 1: its V tile has had a round's time to arrive
+      if (r > 0) {  // round r - 1: its V tile has had this round's scores to arrive
         rescale(a_prev[0], a_prev[1]);
-        if (kept_prev) {
-          const int u = (r - 1) & 1, left = Lb - (j0 + t - W) * kPgTile;
-          mbar_wait(vfull(u * W + warp), (v_phase >> u) & 1, abort_flag);
-          v_phase ^= 1u << u;
-          const uint8_t* vrec = smem + C::kV + (u * W + warp) * C::kTileBytes;
-          const float* sb = sbuf + u * kPgTile * 8;
-#pragma unroll 1
-          for (int i = 0; i < 4 && i * 16 < left; ++i) {
-            const float2 x0 = *reinterpret_cast<const float2*>(sb + (i * 16 + g) * 8 + 2 * c);
-            const float2 x1 = *reinterpret_cast<const float2*>(sb + (i * 16 + g + 8) * 8 + 2 * c);
+        if (kept_prev && v_inflight && await(bars + 8, v_parity)) {
+          v_inflight = false;
+          v_parity ^= 1;
+          const int left = keys - (u - W) * UNIT;
+          const float* sb = sbuf + ((r - 1) & 1) * SB + g * 8 + 2 * c;
+          auto record = [&](auto tail, int i) {
+            const float2 x0 = *reinterpret_cast<const float2*>(sb + i * 128);
+            const float2 x1 = *reinterpret_cast<const float2*>(sb + i * 128 + 64);
             float pr[4];
-            pr[0] = ex2_approx(fmaf(x0.x, sl, -m_prev[0]));
-            pr[1] = ex2_approx(fmaf(x0.y, sl, -m_prev[1]));
-            pr[2] = ex2_approx(fmaf(x1.x, sl, -m_prev[0]));
-            pr[3] = ex2_approx(fmaf(x1.y, sl, -m_prev[1]));
+            pr[0] = ex2_approx(fmaf(x0.x, sl, kP4Log - m_prev[0]));
+            pr[1] = ex2_approx(fmaf(x0.y, sl, kP4Log - m_prev[1]));
+            pr[2] = ex2_approx(fmaf(x1.x, sl, kP4Log - m_prev[0]));
+            pr[3] = ex2_approx(fmaf(x1.y, sl, kP4Log - m_prev[1]));
             l[0] += pr[0] + pr[2];
             l[1] += pr[1] + pr[3];
-            accumulate(vrec + i * REC, left - i * 16, pr);
+            accumulate(tail, vbuf + i * REC, left - i * 16, pr);
+          };
+          if (left >= UNIT) {
+#pragma unroll 1
+            for (int i = 0; i < NREC; ++i) record(full, i);
+          } else {
+#pragma unroll 1
+            for (int i = 0; i * 16 < left; ++i) record(part, i);
           }
+          __syncwarp();
         }
+      }
+      if (keep && !v_inflight) {
+        fetch(key0 + u * UNIT, vkey, vpage, 2, 0, bars + 8);
+        v_inflight = true;
       }
       kept_prev = keep;
 #pragma unroll
       for (int h = 0; h < 2; ++h) { a_prev[h] = a[h]; m_prev[h] = mm[h]; }
     }
+    {  // a wait gave up: wait out this warp's copies before the CTA exits
+      int no_abort = 0;
+      if (k_inflight) mbar_wait(bars, k_count & 1, &no_abort);
+      if (v_inflight) mbar_wait(bars + 8, v_parity, &no_abort);
+    }
   }
 
+  __syncthreads();  // every warp is past its last use of the slots
+  if (*abort_flag) return;
+
   // ---- merge the warps; write the split.
+  auto sum_keys = [&](float x) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+    for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+  };
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
 #pragma unroll
     for (int gr = 0; gr < NG; ++gr)
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1)
-        zacc[gr][i] += __shfl_xor_sync(0xffffffffu, zacc[gr][i], o);
-  __syncthreads();  // with the producer: every warp is past its last use of the rings
-  if (*abort_flag) {
-    if (SKIP && lane == 0) {
-      int no_abort = 0;
-      for (int u = 0; u < 2; ++u)
-        if ((v_used >> u) & 1) mbar_wait(vfull(u * W + warp), ((v_par >> u) & 1) ^ 1, &no_abort);
-    }
-    return;
+      zacc[gr][h] = sum_keys(zacc[gr][h]) - eight[gr][h] * kP4PerUnit * kP4Up;
+    l[h] = sum_keys(l[h]);
+    m[h] -= kP4Log;  // what l, zacc and the codes' part are relative to
   }
   paged_merge_warps<D, W>(
       p, reinterpret_cast<float*>(smem), reinterpret_cast<float2*>(smem + C::kStat), head0, split,
       tid, m, l, [&](int mt, int i) {
+        // 2^133 in two steps; the odd rows' codes came 16 times too large
+        const float o = acc[mt][i] * kP4PerUnit * ((i >> 1) ? kP4Up / 16.f : kP4Up);
         return PagedCell{(mt >> 1) * 32 + 4 * g + 2 * (mt & 1) + (i >> 1),
-                         acc[mt][i] + zacc[mt >> 1][i & 1]};
+                         o + zacc[mt >> 1][i & 1]};
       });
   if (lane == 0 && p.counts) {
     atomicAdd(&p.counts[0], (unsigned long long)n_skipped);

@@ -144,20 +144,17 @@ struct PagedCell {
   float x;
 };
 
-// Merge W warps' O^T, references m (log2 units) and per-lane row sums l of
-// heads 2 c, 2 c + 1, and write the split, or the result when it is the only
+// Merge W warps' O^T, references m (log2 units) and row sums l of heads 2 c,
+// 2 c + 1 (the same at every g), and write the split, or the result when it is the only
 // one.  cell(mt, i): column and value of accumulator i of row tile mt.  red:
 // W * 8 * (D + 4) floats of shared memory that nothing else uses any more.
 template <int D, int W, typename Cell>
 __device__ __forceinline__ void paged_merge_warps(const PagedDecodeParams& p, float* red,
                                                   float2* stat, size_t head0, int split, int tid,
-                                                  const float (&m)[2], float (&l)[2], Cell cell) {
+                                                  const float (&m)[2], const float (&l)[2],
+                                                  Cell cell) {
   constexpr int RS = D + 4;  // row stride of the merge buffer: spreads the banks
   const int warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int o = 4; o < 32; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
 #pragma unroll
   for (int mt = 0; mt < D / 16; ++mt)
 #pragma unroll
@@ -508,6 +505,10 @@ __global__ void __launch_bounds__(kPgThreads, PagedCfg<D>::kCtas)
   }
 
   // ---- merge the warps; write the split.
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
   __syncthreads();  // with the producer: every warp is past its last use of the rings
   if (*abort_flag) {
     if (SKIP && tid == 0) {
