@@ -19,6 +19,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -120,18 +121,14 @@ def _load(path: str) -> ctypes.CDLL:
                                   [I, I, I, F, F, F, P])
     L.sskip_attn_decode_noalloc.restype = I
     L.sskip_attn_decode_noalloc.argtypes = [P, P, P, P, P, P, I, I, I, I, I, F, F, I, I, P, P]
-    LL = ctypes.c_longlong
     L.sskip_kv_page_bytes.restype = Z
     L.sskip_kv_page_bytes.argtypes = [I, I, I, I]
     L.sskip_rope_freqs.restype = I
     L.sskip_rope_freqs.argtypes = [I, D, I, D, D, D, D, P, P]
-    L.sskip_kv_append.restype = I
-    L.sskip_kv_append.argtypes = ([P, P, P, LL, LL, LL, P, P, P, P, F, P, I, I, F, P, P, P, I] +
-                                  [P, P, P, I, I, I, I, I, I, I, I, I, P])
-    L.sskip_kv_gather.restype = I
-    L.sskip_kv_gather.argtypes = [P] * 7 + [I] * 8 + [I, P]
-    L.sskip_attn_decode_paged.restype = I
-    L.sskip_attn_decode_paged.argtypes = [P] * 7 + [I] * 8 + [F, F, I, P, Z, P, P, P]
+    # One packed struct and a stream (see the structs in the header).
+    for f in (L.sskip_kv_append, L.sskip_kv_gather, L.sskip_attn_decode_paged):
+        f.restype = I
+        f.argtypes = [ctypes.c_char_p, P]
     L.sskip_get_status.restype = I
     L.sskip_get_status.argtypes = [P]
     L.sskip_selftest_watchdog.restype = I
@@ -598,89 +595,119 @@ def sskip_rope_freqs(rot_dim: int, base: float, *, scaling: str = "plain", facto
     return turns, attn.value
 
 
+# The argument structs of the header, packed in one step: sskip_paged_cache,
+# then the call's own fields.
+_CACHE = "3P5i4x"
+_APPEND_ARGS = struct.Struct(_CACHE + "11P3q7i2f4x")
+_GATHER_ARGS = struct.Struct(_CACHE + "4P4i")
+_DECODE_ARGS = struct.Struct(_CACHE + "5PN2P4i2f")
+_NO_CACHE = (0, 0, 0, 0, 0, 0, 0, 0)
+
+
 def _addr(t):
-    return None if t is None else t.data_ptr()
+    return 0 if t is None else t.data_ptr()
 
 
-class _on_device:
-    """The device of a call's tensors, made current for its length, and the
-    stream the call launches on."""
-
-    def __init__(self, device, stream):
-        if device.type != "cuda":
-            raise ValueError("expected CUDA tensors")
-        self.device, self.stream = device, stream
-
-    def __enter__(self):
-        self.before = torch.cuda.current_device()
-        if self.before != self.device.index:
-            torch.cuda.set_device(self.device)
-        if self.stream is None:
-            return torch.cuda.current_stream(self.device).cuda_stream
-        return (self.stream.cuda_stream if hasattr(self.stream, "cuda_stream")
-                else int(self.stream))
-
-    def __exit__(self, *exc):
-        if self.before != self.device.index:
-            torch.cuda.set_device(self.before)
+def _launch(fn, args: bytes, dev: int, stream, what: str) -> None:
+    """Call fn on `stream` (default: the device's current one) with the
+    tensors' device current for the length of the call."""
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
+        rc = fn(args, int(stream))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(args, int(stream))
+    if rc != SSKIP_OK:
+        raise SSkipError(rc, what)
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
+def _one_device(*tensors) -> int:
+    """The device index that all the given tensors (None: left out) are on."""
+    dev = -1
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()
+            if d < 0:
+                raise ValueError("expected CUDA tensors")
+            if dev < 0:
+                dev = d
+            elif d != dev:
+                raise ValueError(f"tensors on devices {dev} and {d}")
+    return dev
 
 
 def _pages(k_pages, v_pages, block_table, d):
-    """(format, num_pages, Hkv, page_size, B, max_pages) of a paged cache:
-    bf16 [num_pages, Hkv, page_size, d] or uint8 [num_pages, Hkv,
-    page_size // 16, 10 * d] pages and an int32 [B, max_pages] block table."""
-    if k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype or k_pages.dim() != 4:
+    """(k, v, table address, format, num_pages, page_size, max_pages, B) and
+    Hkv of a paged cache: bf16 [num_pages, Hkv, page_size, d] or uint8
+    [num_pages, Hkv, page_size // 16, 10 * d] pages and an int32
+    [B, max_pages] block table."""
+    if k_pages is None or v_pages is None or block_table is None:
+        raise ValueError("a cache needs k_pages, v_pages and block_table")
+    shape, dtype = k_pages.shape, k_pages.dtype
+    if v_pages.shape != shape or v_pages.dtype != dtype or len(shape) != 4:
         raise ValueError("k_pages and v_pages must be 4-D and of one shape and dtype")
     if not (k_pages.is_contiguous() and v_pages.is_contiguous() and block_table.is_contiguous()):
         raise ValueError("pages and block table must be contiguous")
     if block_table.dtype != torch.int32 or block_table.dim() != 2:
         raise TypeError("block_table must be a 2-D int32 tensor")
-    N, Hkv, rows, width = k_pages.shape
-    if k_pages.dtype == torch.uint8:
+    N, Hkv, rows, width = shape
+    B, M = block_table.shape
+    if dtype == torch.uint8:
         if width != 10 * d:
             raise ValueError(f"4-bit records of d = {d} hold {10 * d} bytes, got {width}")
-        return SSKIP_KV_INT4, N, Hkv, rows * 16, block_table.shape[0], block_table.shape[1]
-    if k_pages.dtype != torch.bfloat16:
-        raise TypeError(f"pages must be bf16, or uint8 records, got {k_pages.dtype}")
-    if width != d:
-        raise ValueError(f"pages hold rows of {width}, expected d = {d}")
-    return SSKIP_KV_BF16, N, Hkv, rows, block_table.shape[0], block_table.shape[1]
+        fmt, rows = SSKIP_KV_INT4, rows * 16
+    elif dtype == torch.bfloat16:
+        if width != d:
+            raise ValueError(f"pages hold rows of {width}, expected d = {d}")
+        fmt = SSKIP_KV_BF16
+    else:
+        raise TypeError(f"pages must be bf16, or uint8 records, got {dtype}")
+    return (k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), fmt, N, rows, M,
+            B), Hkv
 
 
 def _token_rows(t, what):
-    """[T, H, d] bf16, heads packed, any stride between tokens (one token's
-    stride means nothing)."""
+    """[T, H, d] bf16, heads packed, any stride between tokens: that stride (a
+    single token's means nothing)."""
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{what} must be bf16, got {t.dtype}")
     T, H, d = t.shape
-    if t.stride(2) != 1 or (H > 1 and t.stride(1) != d):
+    st, sh, sd = t.stride()
+    if sd != 1 or (sh != d and H > 1):
         raise ValueError(f"{what}: the heads of a token must be packed")
-    return H * d if T <= 1 else t.stride(0)
+    return H * d if T <= 1 else st
 
 
 def _tokens(t, T, what):
-    if t is not None:
-        if t.dtype != torch.int32 or not t.is_contiguous():
-            raise TypeError(f"{what} must be contiguous int32")
-        if t.numel() != T:
-            raise ValueError(f"{what} needs {T} entries")
-    return t
+    if t is None:
+        return 0
+    if t.dtype != torch.int32 or not t.is_contiguous():
+        raise TypeError(f"{what} must be contiguous int32")
+    if t.numel() != T:
+        raise ValueError(f"{what} needs {T} entries")
+    return t.data_ptr()
 
 
 def _rows_out(t, T, H, d, what):
     """out_len of a [T // out_len, H, out_len, d] (or [T, H, d]) output."""
     if t.dtype != torch.bfloat16 or not t.is_contiguous():
         raise TypeError(f"{what} must be contiguous bf16")
-    out_len = 1 if t.dim() == 3 else t.shape[2]
-    if t.numel() != T * H * d or t.shape[1] != H or t.shape[-1] != d:
+    shape = t.shape
+    out_len = 1 if len(shape) == 3 else shape[2]
+    if shape[0] * out_len != T or shape[1] != H or shape[-1] != d or len(shape) not in (3, 4):
         raise ValueError(f"{what} must be [T / out_len, {H}, out_len, {d}] with T = {T}")
     return out_len
+
+
+def _weight(t, d, what):
+    if t is None:
+        return 0
+    if t.dtype != torch.bfloat16 or not t.is_contiguous() or t.numel() != d:
+        raise TypeError(f"{what} must be contiguous bf16 of {d} values")
+    return t.data_ptr()
 
 
 def sskip_kv_append(q, k, v, seq_ids, positions, *, q_out=None, k_out=None, v_out=None,
@@ -691,66 +718,56 @@ def sskip_kv_append(q, k, v, seq_ids, positions, *, q_out=None, k_out=None, v_ou
     seq_ids and positions [T] int32, the norm weights [d] bf16, the int64
     turns table [rot_dim // 2], outputs [T // out_len, H, out_len, d] (or
     [T, H, d]) and a paged cache into sskip_kv_append."""
-    ref = q if q is not None else k
-    T, _, d = ref.shape
-    Hq = 0 if q is None else q.shape[1]
-    Hkv = 0 if k is None else k.shape[1]
-    if (k is None) != (v is None) or (k is not None and k.shape != v.shape) or \
-            (q is not None and k is not None and (k.shape[0] != T or k.shape[2] != d)):
-        raise ValueError("q, k and v must have one T and d, k and v one shape")
-    dev = ref.device
-    _same_device(dev, q=q, k=k, v=v, seq_ids=seq_ids, positions=positions, q_out=q_out,
-                 k_out=k_out, v_out=v_out, k_pages=k_pages, v_pages=v_pages,
-                 block_table=block_table, turns=turns, q_weight=q_weight, k_weight=k_weight)
-    qs = 0 if q is None else _token_rows(q, "q")
-    ks, vs = (0, 0) if k is None else (_token_rows(k, "k"), _token_rows(v, "v"))
-    _tokens(seq_ids, T, "seq_ids")
-    _tokens(positions, T, "positions")
-    lens = {_rows_out(t, T, H, d, n) for t, H, n in ((q_out, Hq, "q_out"), (k_out, Hkv, "k_out"),
-                                                     (v_out, Hkv, "v_out")) if t is not None}
-    if len(lens) > 1:
-        raise ValueError("q_out, k_out and v_out must share one layout")
-    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None and (w.dtype != torch.bfloat16 or not w.is_contiguous() or
-                              w.numel() != d):
-            raise TypeError(f"{n} must be contiguous bf16 of {d} values")
-    if turns is not None and (turns.dtype != torch.int64 or not turns.is_contiguous()):
+    dev = _one_device(q, k, v, seq_ids, positions, q_out, k_out, v_out, k_pages, v_pages,
+                      block_table, turns, q_weight, k_weight)
+    T, _, d = (q if q is not None else k).shape
+    Hq = Hkv = qs = ks = vs = 0
+    if q is not None:
+        Hq, qs = q.shape[1], _token_rows(q, "q")
+    if k is not None or v is not None:
+        if k is None or v is None or k.shape != v.shape or k.shape[0] != T or k.shape[2] != d:
+            raise ValueError("q, k and v must have one T and d, k and v one shape")
+        Hkv, ks, vs = k.shape[1], _token_rows(k, "k"), _token_rows(v, "v")
+    out_len = 0
+    for t, H, n in ((q_out, Hq, "q_out"), (k_out, Hkv, "k_out"), (v_out, Hkv, "v_out")):
+        if t is not None:
+            L = _rows_out(t, T, H, d, n)
+            if out_len and L != out_len:
+                raise ValueError("q_out, k_out and v_out must share one layout")
+            out_len = L
+    if turns is None:
+        rot, turns_at = 0, 0
+    elif turns.dtype != torch.int64 or not turns.is_contiguous():
         raise TypeError("turns must be contiguous int64")
-    fmt = N = P = B = M = 0
+    else:
+        rot, turns_at = 2 * turns.numel(), turns.data_ptr()
+    cache = _NO_CACHE
     if k_pages is not None or v_pages is not None:
-        if k_pages is None or v_pages is None or block_table is None:
-            raise ValueError("a cache needs k_pages, v_pages and block_table")
-        fmt, N, heads, P, B, M = _pages(k_pages, v_pages, block_table, d)
+        cache, heads = _pages(k_pages, v_pages, block_table, d)
         if heads != Hkv:
             raise ValueError(f"the pages hold {heads} heads, k and v {Hkv}")
-    with _on_device(dev, stream) as st:
-        rc = lib().sskip_kv_append(
-            _addr(q), _addr(k), _addr(v), qs, ks, vs, _addr(seq_ids), _addr(positions),
-            _addr(q_weight), _addr(k_weight), eps, _addr(turns),
-            0 if turns is None else 2 * turns.numel(), int(bool(interleaved)), attn_factor,
-            _addr(q_out), _addr(k_out), _addr(v_out), max(lens) if lens else 1, _addr(k_pages),
-            _addr(v_pages), _addr(block_table), fmt, N, P, M, T, B, Hq, Hkv, d, st)
-    _check(rc, "sskip_kv_append")
+    args = _APPEND_ARGS.pack(
+        *cache, _addr(q), _addr(k), _addr(v), _tokens(seq_ids, T, "seq_ids"),
+        _tokens(positions, T, "positions"), _weight(q_weight, d, "q_weight"),
+        _weight(k_weight, d, "k_weight"), turns_at, _addr(q_out), _addr(k_out), _addr(v_out), qs,
+        ks, vs, T, Hq, Hkv, d, rot, 1 if interleaved else 0, out_len or 1, eps, attn_factor)
+    _launch(lib().sskip_kv_append, args, dev, stream, "sskip_kv_append")
 
 
 def sskip_kv_gather(k_pages, v_pages, block_table, seq_ids, positions, k_out, v_out, *,
                     stream=None) -> None:
     """Marshal a paged cache, seq_ids and positions [T] int32 and bf16 outputs
     [T // out_len, Hkv, out_len, d] (or [T, Hkv, d]) into sskip_kv_gather."""
-    dev, d, T = k_pages.device, k_out.shape[-1], seq_ids.numel()
-    _same_device(dev, v_pages=v_pages, block_table=block_table, seq_ids=seq_ids,
-                 positions=positions, k_out=k_out, v_out=v_out)
-    fmt, N, Hkv, P, B, M = _pages(k_pages, v_pages, block_table, d)
-    _tokens(seq_ids, T, "seq_ids")
-    _tokens(positions, T, "positions")
+    dev = _one_device(k_pages, v_pages, block_table, seq_ids, positions, k_out, v_out)
+    d, T = k_out.shape[-1], seq_ids.numel()
+    cache, Hkv = _pages(k_pages, v_pages, block_table, d)
     out_len = _rows_out(k_out, T, Hkv, d, "k_out")
     if _rows_out(v_out, T, Hkv, d, "v_out") != out_len:
         raise ValueError("k_out and v_out must share one layout")
-    with _on_device(dev, stream) as st:
-        rc = lib().sskip_kv_gather(_addr(k_pages), _addr(v_pages), _addr(block_table),
-                                   _addr(seq_ids), _addr(positions), _addr(k_out), _addr(v_out),
-                                   out_len, fmt, N, P, M, T, B, Hkv, d, st)
-    _check(rc, "sskip_kv_gather")
+    args = _GATHER_ARGS.pack(*cache, _tokens(seq_ids, T, "seq_ids"),
+                             _tokens(positions, T, "positions"), k_out.data_ptr(),
+                             v_out.data_ptr(), T, Hkv, d, out_len)
+    _launch(lib().sskip_kv_gather, args, dev, stream, "sskip_kv_gather")
 
 
 def sskip_attn_decode_paged(q, k_pages, v_pages, block_table, seqlens, o, lse, *, sm_scale: float,
@@ -758,30 +775,32 @@ def sskip_attn_decode_paged(q, k_pages, v_pages, block_table, seqlens, o, lse, *
                             skip_count=None, tile_state=None, stream=None) -> None:
     """Marshal q [B,Hq,d] bf16, a paged cache, seqlens [B] int32, o [B,Hq,d]
     bf16, lse [B,Hq] fp32 and a uint8 workspace into sskip_attn_decode_paged."""
-    dev = q.device
-    _same_device(dev, k_pages=k_pages, v_pages=v_pages, block_table=block_table, seqlens=seqlens,
-                 o=o, lse=lse, workspace=workspace, skip_count=skip_count, tile_state=tile_state)
-    B, Hq, d = q.shape
-    fmt, N, Hkv, P, rows, M = _pages(k_pages, v_pages, block_table, d)
+    dev = _one_device(q, k_pages, v_pages, block_table, seqlens, o, lse, workspace, skip_count,
+                      tile_state)
+    shape = q.shape
+    B, Hq, d = shape
+    cache, Hkv = _pages(k_pages, v_pages, block_table, d)
     if q.dtype != torch.bfloat16 or o.dtype != torch.bfloat16:
         raise TypeError("q and o must be bf16")
     if not (q.is_contiguous() and o.is_contiguous() and lse.is_contiguous()):
         raise ValueError("tensors must be contiguous")
-    if o.shape != q.shape or lse.numel() != B * Hq or rows != B:
+    if o.shape != shape or lse.numel() != B * Hq or cache[-1] != B:
         raise ValueError("q, o, lse and block_table must belong to one batch")
     if lse.dtype != torch.float32:
         raise TypeError(f"lse must be float32, got {lse.dtype}")
-    _tokens(seqlens, B, "seqlens")
+    ws_bytes = 0
+    if workspace is not None:
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        ws_bytes = workspace.numel() * workspace.element_size()
     if skip_count is not None:
         _check_counts(skip_count, 2)
     if tile_state is not None:
         _dev(tile_state, torch.uint8, "tile_state")
-        if tile_state.numel() != B * Hkv * (-(-M * P // 64)):
+        if tile_state.numel() != B * Hkv * (-(-cache[6] * cache[5] // 64)):
             raise ValueError("tile_state must be [B, Hkv, ceil(max_pages * page_size / 64)]")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    with _on_device(dev, stream) as st:
-        rc = lib().sskip_attn_decode_paged(
-            _addr(q), _addr(k_pages), _addr(v_pages), _addr(block_table), _addr(seqlens), _addr(o),
-            _addr(lse), fmt, B, Hq, Hkv, N, P, M, d, sm_scale, threshold_scale_factor, num_splits,
-            _addr(workspace), ws_bytes, _addr(skip_count), _addr(tile_state), st)
-    _check(rc, "sskip_attn_decode_paged")
+    args = _DECODE_ARGS.pack(
+        *cache, q.data_ptr(), _tokens(seqlens, B, "seqlens"), o.data_ptr(), lse.data_ptr(),
+        _addr(workspace), ws_bytes, _addr(skip_count), _addr(tile_state), Hq, Hkv, d, num_splits,
+        sm_scale, threshold_scale_factor)
+    _launch(lib().sskip_attn_decode_paged, args, dev, stream, "sskip_attn_decode_paged")

@@ -777,8 +777,11 @@ bool misaligned(const void* p, uintptr_t mask) {
 }
 
 // The host checks every call over a paged cache makes.
-int paged_check(const void* k_pages, const void* v_pages, const int* block_table, int kv_format,
-                int num_pages, int page_size, int max_pages, int B, int Hkv, int d) {
+int paged_check(const sskip_paged_cache& c, int Hkv, int d) {
+  const void *k_pages = c.k_pages, *v_pages = c.v_pages;
+  const int *block_table = c.block_table;
+  const int kv_format = c.kv_format, num_pages = c.num_pages, page_size = c.page_size,
+            max_pages = c.max_pages, B = c.B;
   if (!k_pages || !v_pages || k_pages == v_pages || !block_table) return SSKIP_ERR_INVALID_ARG;
   if (!aligned16(k_pages) || !aligned16(v_pages) || misaligned(block_table, 3))
     return SSKIP_ERR_INVALID_ARG;
@@ -795,14 +798,13 @@ int paged_check(const void* k_pages, const void* v_pages, const int* block_table
   return SSKIP_OK;
 }
 
-PagedRows paged_rows(void* k_pages, void* v_pages, const int* block_table, int num_pages,
-                     int page_size, int max_pages, int B, int Hkv) {
+PagedRows paged_rows(const sskip_paged_cache& a, int Hkv) {
   PagedRows c{};
-  c.k_pages = static_cast<uint8_t*>(k_pages);
-  c.v_pages = static_cast<uint8_t*>(v_pages);
-  c.block_table = block_table;
-  c.B = B; c.Hkv = Hkv; c.num_pages = num_pages; c.max_pages = max_pages;
-  while ((1 << c.page_shift) < page_size) ++c.page_shift;
+  c.k_pages = static_cast<uint8_t*>(a.k_pages);
+  c.v_pages = static_cast<uint8_t*>(a.v_pages);
+  c.block_table = a.block_table;
+  c.B = a.B; c.Hkv = Hkv; c.num_pages = a.num_pages; c.max_pages = a.max_pages;
+  while ((1 << c.page_shift) < a.page_size) ++c.page_shift;
   return c;
 }
 
@@ -916,14 +918,19 @@ SSKIP_API int sskip_rope_freqs(int rot_dim, double base, int scaling, double fac
   return SSKIP_OK;
 }
 
-SSKIP_API int sskip_kv_append(const void* q, const void* k, const void* v, long long q_stride,
-                              long long k_stride, long long v_stride, const int* seq_ids,
-                              const int* positions, const void* q_weight, const void* k_weight,
-                              float eps, const uint64_t* turns, int rot_dim, int interleaved,
-                              float attn_factor, void* q_out, void* k_out, void* v_out,
-                              int out_len, void* k_pages, void* v_pages, const int* block_table,
-                              int kv_format, int num_pages, int page_size, int max_pages, int T,
-                              int B, int Hq, int Hkv, int d, void* stream) {
+SSKIP_API int sskip_kv_append(const sskip_kv_append_args* args, void* stream) {
+  if (!args) return SSKIP_ERR_INVALID_ARG;
+  const sskip_kv_append_args& a = *args;
+  const void *q = a.q, *k = a.k, *v = a.v;
+  void *q_out = a.q_out, *k_out = a.k_out, *v_out = a.v_out;
+  void *k_pages = a.cache.k_pages, *v_pages = a.cache.v_pages;
+  const long long q_stride = a.q_stride, k_stride = a.k_stride, v_stride = a.v_stride;
+  const int *seq_ids = a.seq_ids, *positions = a.positions;
+  const void *q_weight = a.q_weight, *k_weight = a.k_weight;
+  const uint64_t* turns = a.turns;
+  const int T = a.T, Hq = a.Hq, Hkv = a.Hkv, d = a.d, rot_dim = a.rot_dim, out_len = a.out_len,
+            interleaved = a.interleaved;
+  const float eps = a.eps, attn_factor = a.attn_factor;
   if (T < 0 || Hq < 0 || Hkv < 0 || Hq + Hkv < 1 || out_len < 1) return SSKIP_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return SSKIP_ERR_UNSUPPORTED;
   if (rot_dim < 0 || rot_dim > d || !std::isfinite(attn_factor)) return SSKIP_ERR_INVALID_ARG;
@@ -948,8 +955,7 @@ SSKIP_API int sskip_kv_append(const void* q, const void* k, const void* v, long 
                v_stride < (long long)Hkv * d || v_stride % 8)))
     return SSKIP_ERR_INVALID_ARG;
   if (cached) {
-    const int rc = paged_check(k_pages, v_pages, block_table, kv_format, num_pages, page_size,
-                               max_pages, B, Hkv, d);
+    const int rc = paged_check(a.cache, Hkv, d);
     if (rc != SSKIP_OK) return rc;
   }
   const int units = Hq + 2 * Hkv, heads = 32 / (d / 16);
@@ -962,7 +968,9 @@ SSKIP_API int sskip_kv_append(const void* q, const void* k, const void* v, long 
     struct Range { const void* p; size_t n; bool out; };
     const size_t qn = (size_t)T * Hq * d * 2, kn = (size_t)T * Hkv * d * 2;
     auto span = [&](long long stride, int H) { return ((size_t)(T - 1) * stride + (size_t)H * d) * 2; };
-    const size_t pages = cached ? num_pages * sskip_kv_page_bytes(kv_format, Hkv, page_size, d) : 0;
+    const size_t pages =
+        cached ? a.cache.num_pages * sskip_kv_page_bytes(a.cache.kv_format, Hkv, a.cache.page_size, d)
+               : 0;
     const Range r[] = {{q, Hq ? span(q_stride, Hq) : 0, false}, {k, Hkv ? span(k_stride, Hkv) : 0, false},
                        {v, Hkv ? span(v_stride, Hkv) : 0, false}, {q_out, qn, true},
                        {k_out, kn, true}, {v_out, kn, true}, {k_pages, pages, true},
@@ -990,12 +998,11 @@ SSKIP_API int sskip_kv_append(const void* q, const void* k, const void* v, long 
   p.k_out = static_cast<__nv_bfloat16*>(k_out);
   p.v_out = static_cast<__nv_bfloat16*>(v_out);
   p.out_len = out_len; p.T = T; p.Hq = Hq; p.warps_per_token = wpt;
-  if (cached)
-    p.c = paged_rows(k_pages, v_pages, block_table, num_pages, page_size, max_pages, B, Hkv);
+  if (cached) p.c = paged_rows(a.cache, Hkv);
   p.c.Hkv = Hkv;
   const unsigned grid = (unsigned)((warps + kKvThreads / 32 - 1) / (kKvThreads / 32));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const bool q4 = cached && kv_format == SSKIP_KV_INT4;
+  const bool q4 = cached && a.cache.kv_format == SSKIP_KV_INT4;
   if (d == 128) {
     if (q4) kv_append_kernel<128, true><<<grid, kKvThreads, 0, st>>>(p);
     else kv_append_kernel<128, false><<<grid, kKvThreads, 0, st>>>(p);
@@ -1006,13 +1013,15 @@ SSKIP_API int sskip_kv_append(const void* q, const void* k, const void* v, long 
   return cudaGetLastError() == cudaSuccess ? SSKIP_OK : SSKIP_ERR_CUDA;
 }
 
-SSKIP_API int sskip_kv_gather(const void* k_pages, const void* v_pages, const int* block_table,
-                              const int* seq_ids, const int* positions, void* k_out, void* v_out,
-                              int out_len, int kv_format, int num_pages, int page_size,
-                              int max_pages, int T, int B, int Hkv, int d, void* stream) {
+SSKIP_API int sskip_kv_gather(const sskip_kv_gather_args* args, void* stream) {
+  if (!args) return SSKIP_ERR_INVALID_ARG;
+  const sskip_kv_gather_args& a = *args;
+  const int *seq_ids = a.seq_ids, *positions = a.positions;
+  void *k_out = a.k_out, *v_out = a.v_out;
+  const void *k_pages = a.cache.k_pages, *v_pages = a.cache.v_pages;
+  const int T = a.T, Hkv = a.Hkv, d = a.d, out_len = a.out_len, kv_format = a.cache.kv_format;
   if (T < 0 || out_len < 1) return SSKIP_ERR_INVALID_ARG;
-  int rc = paged_check(k_pages, v_pages, block_table, kv_format, num_pages, page_size, max_pages,
-                       B, Hkv, d);
+  const int rc = paged_check(a.cache, Hkv, d);
   if (rc != SSKIP_OK || T == 0) return rc;
   if (T % out_len != 0 || !seq_ids || !positions || !k_out || !v_out || !aligned16(k_out) ||
       !aligned16(v_out) || misaligned(seq_ids, 3) || misaligned(positions, 3))
@@ -1021,7 +1030,7 @@ SSKIP_API int sskip_kv_gather(const void* k_pages, const void* v_pages, const in
   const long long warps = (long long)T * wpt;
   if (warps > 0x7FFFFFFFll - 8 || Hkv > (1 << 19)) return SSKIP_ERR_UNSUPPORTED;
   const size_t on = (size_t)T * Hkv * d * 2;
-  const size_t pages = num_pages * sskip_kv_page_bytes(kv_format, Hkv, page_size, d);
+  const size_t pages = a.cache.num_pages * sskip_kv_page_bytes(kv_format, Hkv, a.cache.page_size, d);
   if (overlap(k_out, on, v_out, on) || overlap(k_out, on, k_pages, pages) ||
       overlap(k_out, on, v_pages, pages) || overlap(v_out, on, k_pages, pages) ||
       overlap(v_out, on, v_pages, pages))
@@ -1032,8 +1041,7 @@ SSKIP_API int sskip_kv_gather(const void* k_pages, const void* v_pages, const in
   p.k_out = static_cast<__nv_bfloat16*>(k_out);
   p.v_out = static_cast<__nv_bfloat16*>(v_out);
   p.out_len = out_len; p.T = T; p.warps_per_token = wpt;
-  p.c = paged_rows(const_cast<void*>(k_pages), const_cast<void*>(v_pages), block_table, num_pages,
-                   page_size, max_pages, B, Hkv);
+  p.c = paged_rows(a.cache, Hkv);
   const unsigned grid = (unsigned)((warps + kKvThreads / 32 - 1) / (kKvThreads / 32));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (kv_format == SSKIP_KV_INT4) {
@@ -1046,20 +1054,25 @@ SSKIP_API int sskip_kv_gather(const void* k_pages, const void* v_pages, const in
   return cudaGetLastError() == cudaSuccess ? SSKIP_OK : SSKIP_ERR_CUDA;
 }
 
-SSKIP_API int sskip_attn_decode_paged(const void* q, const void* k_pages, const void* v_pages,
-                                      const int* block_table, const int* seqlens, void* o,
-                                      float* lse, int kv_format, int B, int Hq, int Hkv,
-                                      int num_pages, int page_size, int max_pages, int d,
-                                      float sm_scale, float threshold_scale_factor, int num_splits,
-                                      void* workspace, size_t workspace_bytes,
-                                      unsigned long long* skip_count, uint8_t* tile_state,
-                                      void* stream) {
+SSKIP_API int sskip_attn_decode_paged(const sskip_decode_paged_args* args, void* stream) {
+  if (!args) return SSKIP_ERR_INVALID_ARG;
+  const sskip_decode_paged_args& a = *args;
+  const void *q = a.q, *k_pages = a.cache.k_pages, *v_pages = a.cache.v_pages;
+  const int* seqlens = a.seqlens;
+  void *o = a.o, *workspace = a.workspace;
+  float* lse = a.lse;
+  unsigned long long* skip_count = a.skip_count;
+  uint8_t* tile_state = a.tile_state;
+  const int B = a.cache.B, Hq = a.Hq, Hkv = a.Hkv, d = a.d, num_splits = a.num_splits;
+  const int kv_format = a.cache.kv_format, num_pages = a.cache.num_pages,
+            page_size = a.cache.page_size, max_pages = a.cache.max_pages;
+  const float sm_scale = a.sm_scale, threshold_scale_factor = a.threshold_scale_factor;
+  const size_t workspace_bytes = a.workspace_bytes;
   if (!q || !seqlens || !o || !lse) return SSKIP_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(o) || misaligned(seqlens, 3) || misaligned(lse, 3) ||
       misaligned(workspace, 255) || misaligned(skip_count, 7))
     return SSKIP_ERR_INVALID_ARG;
-  const int rc = paged_check(k_pages, v_pages, block_table, kv_format, num_pages, page_size,
-                             max_pages, B, Hkv, d);
+  const int rc = paged_check(a.cache, Hkv, d);
   if (rc != SSKIP_OK) return rc;
   if (Hq < 1 || Hq % Hkv != 0 || num_splits < 1) return SSKIP_ERR_INVALID_ARG;
   if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return SSKIP_ERR_INVALID_ARG;
@@ -1078,8 +1091,7 @@ SSKIP_API int sskip_attn_decode_paged(const void* q, const void* k_pages, const 
   PagedDecodeParams p{};
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.seqlens = seqlens;
-  p.c = paged_rows(const_cast<void*>(k_pages), const_cast<void*>(v_pages), block_table, num_pages,
-                   page_size, max_pages, B, Hkv);
+  p.c = paged_rows(a.cache, Hkv);
   if (num_splits > 1) {
     p.o_part = static_cast<float*>(workspace);
     p.lse_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + align256(rows * d * 4));

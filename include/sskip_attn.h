@@ -414,6 +414,18 @@ int sskip_permute_rows(const void* src, void* dst, const int32_t* idx, long long
  */
 typedef enum { SSKIP_KV_BF16 = 0, SSKIP_KV_INT4 = 1 } sskip_kv_format;
 
+/* A paged cache, as the calls below take it.  Their arguments come as structs:
+ * a binding fills one in a single step, and no argument can change places with
+ * its neighbour. */
+typedef struct {
+    void* k_pages;
+    void* v_pages;
+    const int* block_table;
+    int kv_format;  /* sskip_kv_format */
+    int num_pages, page_size, max_pages;
+    int B;          /* rows of the block table */
+} sskip_paged_cache;
+
 /* Bytes of one page of keys (or of values); 0 for an unsupported shape. */
 size_t sskip_kv_page_bytes(int kv_format, int Hkv, int page_size, int d);
 
@@ -477,14 +489,19 @@ int sskip_rope_freqs(int rot_dim, double base, int scaling, double factor, doubl
  * SSKIP_KV_INT4) from fp32 to the 4-bit form.  No output may overlap an input
  * or another output.  T = 0 is a call that does nothing.
  */
-int sskip_kv_append(const void* q, const void* k, const void* v, long long q_stride,
-                    long long k_stride, long long v_stride, const int* seq_ids,
-                    const int* positions, const void* q_weight, const void* k_weight, float eps,
-                    const uint64_t* turns, int rot_dim, int interleaved, float attn_factor,
-                    void* q_out, void* k_out, void* v_out, int out_len, void* k_pages,
-                    void* v_pages, const int* block_table, int kv_format, int num_pages,
-                    int page_size, int max_pages, int T, int B, int Hq, int Hkv, int d,
-                    void* stream);
+typedef struct {
+    sskip_paged_cache cache;  /* k_pages = v_pages = NULL: no cache */
+    const void *q, *k, *v;
+    const int *seq_ids, *positions;
+    const void *q_weight, *k_weight;
+    const uint64_t* turns;
+    void *q_out, *k_out, *v_out;
+    long long q_stride, k_stride, v_stride;
+    int T, Hq, Hkv, d, rot_dim, interleaved, out_len;
+    float eps, attn_factor;
+} sskip_kv_append_args;
+
+int sskip_kv_append(const sskip_kv_append_args* args, void* stream);
 
 /*
  * Rows of the cache back as bf16: for T tokens (seq_ids, positions as above;
@@ -494,10 +511,14 @@ int sskip_kv_append(const void* q, const void* k, const void* v, long long q_str
  * values are computed in fp32 and rounded once to bf16.  The same token may be
  * asked for several times.  T = 0 does nothing.
  */
-int sskip_kv_gather(const void* k_pages, const void* v_pages, const int* block_table,
-                    const int* seq_ids, const int* positions, void* k_out, void* v_out,
-                    int out_len, int kv_format, int num_pages, int page_size, int max_pages, int T,
-                    int B, int Hkv, int d, void* stream);
+typedef struct {
+    sskip_paged_cache cache;
+    const int *seq_ids, *positions;
+    void *k_out, *v_out;
+    int T, Hkv, d, out_len;
+} sskip_kv_gather_args;
+
+int sskip_kv_gather(const sskip_kv_gather_args* args, void* stream);
 
 /*
  * Decode over a paged cache: sskip_attn_decode's rule (decode tiles of 64 keys
@@ -522,12 +543,21 @@ int sskip_kv_gather(const void* k_pages, const void* v_pages, const int* block_t
  * P is rounded to bf16 for its product with V, the row sum is not; in the
  * 4-bit form the value's scale joins P before that rounding.
  */
-int sskip_attn_decode_paged(const void* q, const void* k_pages, const void* v_pages,
-                            const int* block_table, const int* seqlens, void* o, float* lse,
-                            int kv_format, int B, int Hq, int Hkv, int num_pages, int page_size,
-                            int max_pages, int d, float sm_scale, float threshold_scale_factor,
-                            int num_splits, void* workspace, size_t workspace_bytes,
-                            unsigned long long* skip_count, uint8_t* tile_state, void* stream);
+typedef struct {
+    sskip_paged_cache cache;  /* one row of the block table a sequence */
+    const void* q;
+    const int* seqlens;
+    void* o;
+    float* lse;
+    void* workspace;
+    size_t workspace_bytes;
+    unsigned long long* skip_count;
+    uint8_t* tile_state;
+    int Hq, Hkv, d, num_splits;
+    float sm_scale, threshold_scale_factor;
+} sskip_decode_paged_args;
+
+int sskip_attn_decode_paged(const sskip_decode_paged_args* args, void* stream);
 
 /*
  * Synchronises `stream`, then returns and clears the current device's status

@@ -26,16 +26,57 @@ def at(i, off=0):
     return ctypes.c_void_p((i + 1) * GB + off)
 
 
+P, I, F, LL = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_longlong
+
+
+class Cache(ctypes.Structure):
+    _fields_ = [("kp", P), ("vp", P), ("table", P)] + [(n, I) for n in ("fmt", "N", "P", "M", "B")]
+
+
+class AppendArgs(ctypes.Structure):
+    _fields_ = ([("cache", Cache)] +
+                [(n, P) for n in ("q", "k", "v", "seq", "pos", "qw", "kw", "turns", "qo", "ko", "vo")] +
+                [(n, LL) for n in ("qs", "ks", "vs")] +
+                [(n, I) for n in ("T", "Hq", "Hkv", "d", "rot", "inter", "out_len")] +
+                [("eps", F), ("attn", F)])
+
+
+class GatherArgs(ctypes.Structure):
+    _fields_ = ([("cache", Cache)] + [(n, P) for n in ("seq", "pos", "ko", "vo")] +
+                [(n, I) for n in ("T", "Hkv", "d", "out_len")])
+
+
+class DecodeArgs(ctypes.Structure):
+    _fields_ = ([("cache", Cache)] + [(n, P) for n in ("q", "lens", "o", "lse", "ws")] +
+                [("ws_bytes", ctypes.c_size_t), ("count", P), ("state", P)] +
+                [(n, I) for n in ("Hq", "Hkv", "d", "S")] + [("scale", F), ("tsf", F)])
+
+
+def fill(kind, a):
+    x = kind()
+    for n, v in a.items():
+        owner = x if n in dict(kind._fields_) else x.cache
+        setattr(owner, n, v.value if isinstance(v, P) else v)
+    return bytes(x)
+
+
+def test_the_binding_packs_the_structs_of_the_header():
+    for kind, packed in ((AppendArgs, sk._APPEND_ARGS), (GatherArgs, sk._GATHER_ARGS),
+                         (DecodeArgs, sk._DECODE_ARGS)):
+        assert ctypes.sizeof(kind) == packed.size, kind
+        # every field at its place: fields filled with 1, 2, 3, ... both ways
+        names = [n for n, _ in Cache._fields_] + [n for n, _ in kind._fields_ if n != "cache"]
+        assert fill(kind, {n: i + 1 for i, n in enumerate(names)}) == \
+            packed.pack(*range(1, len(names) + 1))
+
+
 def append(lib, **kw):
     a = dict(q=at(0), k=at(1), v=at(2), qs=8 * 128, ks=2 * 128, vs=2 * 128, seq=at(3), pos=at(4),
              qw=at(5), kw=at(6), eps=1e-6, turns=at(7), rot=128, inter=0, attn=1.0, qo=at(8),
              ko=at(9), vo=at(10), out_len=1, kp=at(11), vp=at(12), table=at(13), fmt=0, N=10, P=64,
              M=4, T=4, B=2, Hq=8, Hkv=2, d=128)
     a.update(kw)
-    return lib.sskip_kv_append(*(a[n] for n in (
-        "q", "k", "v", "qs", "ks", "vs", "seq", "pos", "qw", "kw", "eps", "turns", "rot", "inter",
-        "attn", "qo", "ko", "vo", "out_len", "kp", "vp", "table", "fmt", "N", "P", "M", "T", "B",
-        "Hq", "Hkv", "d")), None)
+    return lib.sskip_kv_append(fill(AppendArgs, a), None)
 
 
 @pytest.mark.parametrize("kw,rc", [
@@ -63,6 +104,8 @@ def test_append_refuses(lib, kw, rc):
 
 def test_calls_without_tokens_do_nothing(lib):
     assert append(lib, T=0) == sk.SSKIP_OK
+    for f in (lib.sskip_kv_append, lib.sskip_kv_gather, lib.sskip_attn_decode_paged):
+        assert f(None, None) == INVALID
     assert append(lib, T=0, q=None, k=None, v=None, qo=None) == sk.SSKIP_OK
     assert gather(lib, T=0) == sk.SSKIP_OK
 
@@ -71,7 +114,7 @@ def gather(lib, **kw):
     a = dict(kp=at(0), vp=at(1), table=at(2), seq=at(3), pos=at(4), ko=at(5), vo=at(6), out_len=1,
              fmt=1, N=10, P=64, M=4, T=4, B=2, Hkv=2, d=64)
     a.update(kw)
-    return lib.sskip_kv_gather(*a.values(), None)
+    return lib.sskip_kv_gather(fill(GatherArgs, a), None)
 
 
 @pytest.mark.parametrize("kw,rc", [
@@ -90,7 +133,7 @@ def decode(lib, **kw):
              Hq=8, Hkv=2, N=10, P=64, M=4, d=128, scale=0.1, tsf=5.0, S=4, ws=at(7),
              ws_bytes=1 << 20, count=None, state=None)
     a.update(kw)
-    return lib.sskip_attn_decode_paged(*a.values(), None)
+    return lib.sskip_attn_decode_paged(fill(DecodeArgs, a), None)
 
 
 @pytest.mark.parametrize("kw,rc", [
@@ -171,12 +214,14 @@ def test_tensor_checks_of_the_binding():
     z = torch.zeros
     bf = torch.bfloat16
     pages, table = z(4, 2, 16, 64, dtype=bf), z(1, 4, dtype=torch.int32)
-    assert sk._pages(pages, pages.clone(), table, 64) == (0, 4, 2, 16, 1, 4)
+    got, heads = sk._pages(pages, pages.clone(), table, 64)
+    assert (got[3:], heads) == ((0, 4, 16, 4, 1), 2)
     rec = z(4, 2, 1, 640, dtype=torch.uint8)
-    assert sk._pages(rec, rec.clone(), table, 64) == (1, 4, 2, 16, 1, 4)
+    got, heads = sk._pages(rec, rec.clone(), table, 64)
+    assert (got[3:], heads) == ((1, 4, 16, 4, 1), 2)
     for a, b, t, d, err in [(pages, pages[:, :1], table, 64, ValueError),
                             (pages, pages.float(), table, 64, ValueError),
-                            (pages.float(), pages.float(), table, 64, TypeError),
+                            (pages.float(), pages.float(), table, 64, TypeError), (pages, None, table, 64, ValueError),
                             (pages, pages, table.long(), 64, TypeError),
                             (pages, pages, table, 128, ValueError), (rec, rec, table, 128, ValueError),
                             (pages.transpose(1, 2), pages.transpose(1, 2), table, 64, ValueError)]:
@@ -202,4 +247,4 @@ def test_tensor_checks_of_the_binding():
     with pytest.raises(ValueError):
         sk._tokens(z(4, dtype=torch.int32), 5, "positions")
     with pytest.raises(ValueError):
-        sk._same_device(torch.device("cuda", 0), q=qkv)
+        sk._one_device(None, qkv)
