@@ -4,9 +4,8 @@
 //   mn = min rounded down, sc = (max - mn) / 15 rounded up, n = rint((x - mn) / sc)
 // clamped to 0 .. 15, and the value read back is sc n + mn.  Rounding mn down
 // and sc up keeps every value inside [mn, mn + 15 sc], so no value is off by
-// more than sc / 2.  The quotients are true divisions: with the bf16 inputs of
-// the values exact ties are common, and they must go to the even code whatever
-// the device.  A group that holds a NaN or an infinity, or whose spread does
+// more than sc / 2.  Codes are those of the exact quotient: with the bf16 inputs
+// of the values exact ties are common, and they go to the even code.  A group that holds a NaN or an infinity, or whose spread does
 // not fit, reads back as NaN.
 //
 // A record is 16 rows of one head: the codes (8 D bytes), then [16][D / 32]
@@ -49,43 +48,79 @@ __device__ __forceinline__ void kv4_bounds(const float (&x)[8], float& lo, float
   }
 }
 
+// rint(y / sc) for 0 <= y <= about 15 sc, ties to even, as the exact quotient
+// gives it: a reciprocal's estimate (off by one at most, next to a tie), put
+// right by the exact remainder.  One division a group instead of one a value:
+// the reciprocal unit takes 8 clocks of a sub-partition for a warp.
+__device__ __forceinline__ uint32_t kv4_code(float y, float sc, float inv) {
+  constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
+  float n = fminf(fmaxf(fmaf(y, inv, kRound) - kRound, 0.f), 15.f);
+  const float rest = fmaf(-n, sc, y), over = fabsf(rest) - 0.5f * sc;
+  const bool odd = (uint32_t)n & 1u;
+  if (over > 0.f || (over == 0.f && odd)) n += rest > 0.f ? 1.f : -1.f;
+  return (uint32_t)fminf(fmaxf(n, 0.f), 15.f);
+}
+
 // Store row r of a record.  The D / 16 lanes of a head hold chunks m0 and m1
-// (8 values each) of it; all 32 lanes call, `live` ones write.
+// (8 values each) of it; all 32 lanes call, `live` ones write.  split: how many
+// lanes of a head hold chunks (j, j + split), which `apart` says of this one;
+// the others hold (2 j, 2 j + 1).
 template <int D>
-__device__ __forceinline__ void kv4_store_row(uint8_t* rec, int r, bool value, bool live, int m0,
-                                              int m1, const float (&x0)[8], const float (&x1)[8]) {
+__device__ __forceinline__ void kv4_store_row(uint8_t* rec, int r, bool value, bool live, int split,
+                                              bool apart, int m0, int m1, const float (&x0)[8],
+                                              const float (&x1)[8]) {
   constexpr int LH = D / 16, NG = Kv4<D>::kGroups;
-  float lo0, hi0, lo1, hi1, glo[2], ghi[2];
-  kv4_bounds(x0, lo0, hi0);
-  kv4_bounds(x1, lo1, hi1);
-  glo[0] = glo[1] = ghi[0] = ghi[1] = 0.f;
-#pragma unroll
-  for (int g = 0; g < NG; ++g) {
-    float lo = fminf((m0 >> 2) == g ? lo0 : INFINITY, (m1 >> 2) == g ? lo1 : INFINITY);
-    float hi = fmaxf((m0 >> 2) == g ? hi0 : -INFINITY, (m1 >> 2) == g ? hi1 : -INFINITY);
-#pragma unroll
-    for (int o = LH / 2; o > 0; o >>= 1) {
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  constexpr uint32_t kAll = 0xffffffffu;
+  float lo[2], hi[2];  // of the groups of the two chunks
+  kv4_bounds(x0, lo[0], hi[0]);
+  kv4_bounds(x1, lo[1], hi[1]);
+  if (split <= 2 || split % 4 == 0) {
+    // A group's four chunks are both chunks of a pair of lanes, or (apart,
+    // split a multiple of 4) one chunk each of four neighbours.
+    const bool quad = apart && split > 2;
+    if (!quad) {
+      lo[0] = lo[1] = fminf(lo[0], lo[1]);
+      hi[0] = hi[1] = fmaxf(hi[0], hi[1]);
     }
-    if ((m0 >> 2) == g) { glo[0] = lo; ghi[0] = hi; }
-    if ((m1 >> 2) == g) { glo[1] = lo; ghi[1] = hi; }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      lo[i] = fminf(lo[i], __shfl_xor_sync(kAll, lo[i], 1));
+      hi[i] = fmaxf(hi[i], __shfl_xor_sync(kAll, hi[i], 1));
+      const float l2 = __shfl_xor_sync(kAll, lo[i], 2), h2 = __shfl_xor_sync(kAll, hi[i], 2);
+      if (quad) {
+        lo[i] = fminf(lo[i], l2);
+        hi[i] = fmaxf(hi[i], h2);
+      }
+    }
+  } else {
+    const float clo[2] = {lo[0], lo[1]}, chi[2] = {hi[0], hi[1]};
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      float l = fminf((m0 >> 2) == g ? clo[0] : INFINITY, (m1 >> 2) == g ? clo[1] : INFINITY);
+      float h = fmaxf((m0 >> 2) == g ? chi[0] : -INFINITY, (m1 >> 2) == g ? chi[1] : -INFINITY);
+#pragma unroll
+      for (int o = LH / 2; o > 0; o >>= 1) {
+        l = fminf(l, __shfl_xor_sync(kAll, l, o));
+        h = fmaxf(h, __shfl_xor_sync(kAll, h, o));
+      }
+      if ((m0 >> 2) == g) { lo[0] = l; hi[0] = h; }
+      if ((m1 >> 2) == g) { lo[1] = l; hi[1] = h; }
+    }
   }
   if (!live) return;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int m = i ? m1 : m0;
-    const __nv_bfloat16 mnb = __float2bfloat16_rd(glo[i]);
-    float mn = __bfloat162float(mnb);
-    float sc = __bfloat162float(__float2bfloat16_ru(__fdiv_rn(ghi[i] - mn, 15.f)));
+    const float mn = __bfloat162float(__float2bfloat16_rd(lo[i]));
+    const float sc = __bfloat162float(__float2bfloat16_ru(__fdiv_rn(hi[i] - mn, 15.f)));
     const bool bad = !(sc <= FLT_MAX) || !(fabsf(mn) <= FLT_MAX);
+    const bool flat = bad || sc == 0.f;
+    const float up = sc < 0x1p-100f ? 0x1p64f : 1.f;  // a reciprocal within fp32 for any scale
+    const float scu = sc * up, inv = __frcp_rn(scu);
     uint32_t n[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float x = i ? x1[e] : x0[e];
-      const float y = rintf(__fdiv_rn(x - mn, sc));
-      n[e] = (sc > 0.f && !bad) ? (uint32_t)fminf(fmaxf(y, 0.f), 15.f) : 0u;
-    }
+    for (int e = 0; e < 8; ++e)
+      n[e] = flat ? 0u : kv4_code(((i ? x1[e] : x0[e]) - mn) * up, scu, inv);
     if ((m & 3) == 0) {
       uint32_t w = bad ? 0x7FFF7FFFu : pack_bf16x2(sc, mn);
       *reinterpret_cast<uint32_t*>(rec + Kv4<D>::kCodes + (r * NG + (m >> 2)) * 4) = w;

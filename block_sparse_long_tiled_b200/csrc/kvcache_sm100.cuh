@@ -18,9 +18,11 @@
 // The work is HBM traffic (a row is read once and written once or twice).
 // D / 16 lanes hold one head's row as two 16-byte pieces a lane; the pieces
 // are chosen so that a lane owns both members of its eight pairs in either
-// pairing, so the rotation needs no exchange.  A warp stays on one token and
-// walks its heads, so a lane computes its eight sines and cosines once for all
-// of them.  Small calls give a token's heads to several warps instead.
+// pairing, so the rotation needs no exchange.  A token's rot / 2 sines and
+// cosines are worked out once, one or two a lane, and shared.  Large calls give
+// a token to one warp, which walks its heads and loads the next rows ahead of
+// the arithmetic of the current ones; small ones give a token a CTA, every
+// group of heads a warp of its own.
 #pragma once
 
 #include <cstdint>
@@ -48,7 +50,7 @@ struct AppendParams {
   int interleaved;
   float attn_factor;
   __nv_bfloat16 *q_out, *k_out, *v_out;    // [T / out_len, H, out_len, D] or null
-  int out_len, T, Hq, warps_per_token;
+  int out_len, T, Hq;
   PagedRows c;
 };
 
@@ -59,7 +61,9 @@ struct GatherParams {
   PagedRows c;
 };
 
-constexpr int kKvThreads = 128;
+constexpr int kKvThreads = 128;      // of a gather
+constexpr int kAppendMaxWarps = 12;  // of a token with a CTA to itself
+constexpr int kAppendAlone = 4;      // tokens of a CTA whose warps have one each
 
 // Page and offset of a token's row; false for a padding token (negative
 // sequence) or an index outside the table, which is latched.
@@ -80,8 +84,8 @@ __device__ __forceinline__ bool locate_row(const PagedRows& c, int seq, int pos,
   return true;
 }
 
-__device__ __forceinline__ void load_chunk(const __nv_bfloat16* p, float (&x)[8]) {
-  bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(p)), x);
+__device__ __forceinline__ uint4 load_raw(const __nv_bfloat16* p) {
+  return __ldg(reinterpret_cast<const uint4*>(p));
 }
 
 __device__ __forceinline__ void store_chunk(__nv_bfloat16* p, const float (&x)[8]) {
@@ -111,70 +115,94 @@ __device__ __forceinline__ void turn_cos_sin(long long pos, unsigned long long t
   s = ss * scale;
 }
 
-template <int D, bool Q4>
-__global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const AppendParams p) {
+// ALONE: a warp has a token to itself (else the CTA has one).
+template <int D, bool Q4, bool ALONE>
+__global__ void __launch_bounds__(ALONE ? kAppendAlone * 32 : kAppendMaxWarps * 32, ALONE ? 8 : 2)
+    kv_append_kernel(const AppendParams p) {
   constexpr int LH = D / 16;       // lanes per head
   constexpr int HW = 32 / LH;      // heads a warp holds at a time
-  const int gw = blockIdx.x * (kKvThreads / 32) + (threadIdx.x >> 5);
-  const int t = gw / p.warps_per_token, part = gw - t * p.warps_per_token;
-  if (t >= p.T) return;
+  // cosine and sine of pair 8 j + e at e LH + j
+  __shared__ float tabs[ALONE ? kAppendAlone : 1][2][D / 2];
   const int lane = threadIdx.x & 31, j = lane % LH, hs = lane / LH;
+  const int warp = ALONE ? 0 : threadIdx.x >> 5, warps = ALONE ? 1 : blockDim.x >> 5;
+  const int t = ALONE ? blockIdx.x * kAppendAlone + (threadIdx.x >> 5) : blockIdx.x;
+  if (ALONE && t >= p.T) return;
+  auto& tab = tabs[ALONE ? threadIdx.x >> 5 : 0];
   const int pos = p.positions ? __ldg(p.positions + t) : 0;
-  int page = 0, off = 0;
-  const bool cached = p.c.k_pages != nullptr;
-  if (cached) {
-    if (!locate_row(p.c, __ldg(p.seq_ids + t), pos, &page, &off)) return;
-  } else if (p.seq_ids && __ldg(p.seq_ids + t) < 0) {
-    return;
-  }
+  const int seq = p.seq_ids ? __ldg(p.seq_ids + t) : 0;
   // The lane's pairs 8 j .. 8 j + 7: in chunks (j, j + rot / 16) when pairs are
   // half the rotated part apart, in (2 j, 2 j + 1) when they are neighbours or
   // not rotated at all.
   const bool turns = j < p.rot_chunks;
-  float cs[8], sn[8];
-  if (turns) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      turn_cos_sin(pos, __ldg(p.turns + 8 * j + e), p.attn_factor, cs[e], sn[e]);
-  }
   const bool apart = turns && !p.interleaved;
   const int m0 = apart ? j : 2 * j, m1 = apart ? j + p.rot_chunks : 2 * j + 1;
-  const size_t ob = (size_t)(t / p.out_len), oi = (size_t)(t % p.out_len);
 
-  const int units = p.Hq + 2 * p.c.Hkv;
-  for (int u0 = part * HW; u0 < units; u0 += p.warps_per_token * HW) {
+  const int Hkv = p.c.Hkv, units = p.Hq + 2 * Hkv;
+  // kind 0: query, 1: key, 2: value
+  auto kind_of = [&](int u) { return u < p.Hq ? 0 : (u < p.Hq + Hkv ? 1 : 2); };
+  auto head_of = [&](int u, int kind) {
+    return kind == 0 ? u : (kind == 1 ? u - p.Hq : u - p.Hq - Hkv);
+  };
+  uint4 r0, r1;
+  auto load = [&](int u) {
+    r0 = r1 = make_uint4(0u, 0u, 0u, 0u);
+    if (u < units) {
+      const int kind = kind_of(u);
+      const __nv_bfloat16* row =
+          (kind == 0 ? p.q + (size_t)t * p.q_stride
+                     : (kind == 1 ? p.k + (size_t)t * p.k_stride : p.v + (size_t)t * p.v_stride)) +
+          (size_t)head_of(u, kind) * D;
+      r0 = load_raw(row + m0 * 8);
+      r1 = load_raw(row + m1 * 8);
+    }
+  };
+  const bool cached = p.c.k_pages != nullptr;
+  if (seq < 0) return;  // padding: all of the token's threads
+  load(warp * HW + hs);
+  int page = 0, off = 0;
+  if (cached && !locate_row(p.c, seq, pos, &page, &off)) return;
+  for (int i = ALONE ? lane : threadIdx.x; i < p.rot_chunks * 8; i += ALONE ? 32 : blockDim.x) {
+    float c, s;
+    turn_cos_sin(pos, __ldg(p.turns + i), p.attn_factor, c, s);
+    tab[0][(i & 7) * LH + (i >> 3)] = c;
+    tab[1][(i & 7) * LH + (i >> 3)] = s;
+  }
+  if (ALONE) __syncwarp();
+  else __syncthreads();
+  float cs[8], sn[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    cs[e] = turns ? tab[0][e * LH + j] : 1.f;
+    sn[e] = turns ? tab[1][e * LH + j] : 0.f;
+  }
+  const size_t ob = (size_t)(t / p.out_len), oi = (size_t)(t % p.out_len);
+  const bool any_norm = p.q_weight || p.k_weight;
+
+  for (int u0 = warp * HW; u0 < units; u0 += warps * HW) {
     const int u = u0 + hs;
     const bool live = u < units;
-    // kind 0: query, 1: key, 2: value
-    const int kind = u < p.Hq ? 0 : (u < p.Hq + p.c.Hkv ? 1 : 2);
-    const int h = kind == 0 ? u : (kind == 1 ? u - p.Hq : u - p.Hq - p.c.Hkv);
+    const int kind = kind_of(u), h = head_of(u, kind);
     float x0[8], x1[8];
+    bf16x8_to_f32(r0, x0);
+    bf16x8_to_f32(r1, x1);
+    load(u + warps * HW);  // the next rows, while these are worked on
+    if (any_norm) {
+      const __nv_bfloat16* w = kind == 0 ? p.q_weight : p.k_weight;
+      float ss = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x0[e] = x1[e] = 0.f;
-    if (live) {
-      const __nv_bfloat16* row =
-          kind == 0 ? p.q + (size_t)t * p.q_stride
-                    : (kind == 1 ? p.k + (size_t)t * p.k_stride : p.v + (size_t)t * p.v_stride);
-      row += (size_t)h * D;
-      load_chunk(row + m0 * 8, x0);
-      load_chunk(row + m1 * 8, x1);
-    }
-    const __nv_bfloat16* w = kind == 0 ? p.q_weight : p.k_weight;
-    const bool norm = live && kind < 2 && w != nullptr;
-    float ss = 0.f;
+      for (int e = 0; e < 8; ++e) ss = fmaf(x0[e], x0[e], fmaf(x1[e], x1[e], ss));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(x0[e], x0[e], fmaf(x1[e], x1[e], ss));
+      for (int o = LH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (kind < 2 && w != nullptr) {
+        const float r = rsqrtf(ss * (1.0f / D) + p.eps);
+        float w0[8], w1[8];
+        bf16x8_to_f32(load_raw(w + m0 * 8), w0);
+        bf16x8_to_f32(load_raw(w + m1 * 8), w1);
 #pragma unroll
-    for (int o = LH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (norm) {
-      const float r = rsqrtf(ss * (1.0f / D) + p.eps);
-      float w0[8], w1[8];
-      load_chunk(w + m0 * 8, w0);
-      load_chunk(w + m1 * 8, w1);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x0[e] = x0[e] * r * w0[e];
-        x1[e] = x1[e] * r * w1[e];
+        for (int e = 0; e < 8; ++e) {
+          x0[e] = x0[e] * r * w0[e];
+          x1[e] = x1[e] * r * w1[e];
+        }
       }
     }
     if (turns && kind < 2) {
@@ -198,7 +226,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const AppendParam
     }
     __nv_bfloat16* out = kind == 0 ? p.q_out : (kind == 1 ? p.k_out : p.v_out);
     if (live && out) {
-      const int H = kind == 0 ? p.Hq : p.c.Hkv;
+      const int H = kind == 0 ? p.Hq : Hkv;
       __nv_bfloat16* o = out + ((ob * H + h) * (size_t)p.out_len + oi) * D;
       store_chunk(o + m0 * 8, x0);
       store_chunk(o + m1 * 8, x1);
@@ -208,14 +236,14 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(const AppendParam
       // a warp with no key or value head has nothing to write.
       if (__any_sync(0xffffffffu, live && kind > 0)) {
         uint8_t* base = kind == 2 ? p.c.v_pages : p.c.k_pages;
-        uint8_t* rec = base + (((size_t)page * p.c.Hkv + (kind == 0 ? 0 : h))
-                                   << (p.c.page_shift - 4)) * Kv4<D>::kRecord +
-                       (size_t)(off >> 4) * Kv4<D>::kRecord;
-        kv4_store_row<D>(rec, off & 15, kind == 2, live && kind > 0, m0, m1, x0, x1);
+        uint8_t* rec = base + ((((size_t)page * Hkv + (kind == 0 ? 0 : h)) << (p.c.page_shift - 4)) +
+                               (off >> 4)) * Kv4<D>::kRecord;
+        kv4_store_row<D>(rec, off & 15, kind == 2, live && kind > 0, p.interleaved ? 0 : p.rot_chunks,
+                         apart, m0, m1, x0, x1);
       }
     } else if (cached && live && kind > 0) {
       __nv_bfloat16* base = reinterpret_cast<__nv_bfloat16*>(kind == 1 ? p.c.k_pages : p.c.v_pages);
-      __nv_bfloat16* o = base + ((((size_t)page * p.c.Hkv + h) << p.c.page_shift) + off) * D;
+      __nv_bfloat16* o = base + ((((size_t)page * Hkv + h) << p.c.page_shift) + off) * D;
       store_chunk(o + m0 * 8, x0);
       store_chunk(o + m1 * 8, x1);
     }
