@@ -58,7 +58,9 @@ struct Paged4Cfg {
   static constexpr int kV = kK + kP4Warps * kSlots * kBytes;
   static constexpr int kS = kV + kP4Warps * kSlots * kBytes;  // [W][2][64][8] fp32 scores
   static constexpr int kMax = kS + (SKIP ? kP4Warps * 2 * kPgTile * 8 * 4 : 0);  // [2][8][W]
-  static constexpr int kMerge = kP4Warps * 8 * (D + 4) * 4;   // reuses the slots and the scores
+  // The two merges reuse the slots and the scores.
+  static constexpr int kPart = kP4Warps * 8 * (D + 4) * 4;
+  static constexpr int kMerge = kPart + (int)sizeof(PagedPart<D>);
   static constexpr int kStat = (kMax > kMerge ? kMax : kMerge) + 2 * 8 * kP4Warps * 4;
   static constexpr int kBar = kStat + kP4Warps * 8 * 8;
   static constexpr int kTotal = kBar + kP4Warps * kBars * 8 + 16;
@@ -125,8 +127,10 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
   const int j0 = split * c_per;
   const int ntiles = max(0, min(n_k, j0 + c_per) - j0);
   const size_t head0 = (size_t)b * p.Hq + (size_t)kvh * p.G;
+  auto* part = reinterpret_cast<PagedPart<D>*>(smem + C::kPart);
   if (ntiles == 0) {
-    paged_empty_split<D>(p, head0, split, tid, kP4Threads);
+    paged_empty_split<D>(p, part, head0, split, tid, kP4Threads);
+    if (p.clustered) paged_cluster_merge<D>(p, part, head0, tid, kP4Threads);
     return;
   }
   const int key0 = j0 * kPgTile;                              // of the split
@@ -256,9 +260,9 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
     eight[i][0] = eight[i][1] = eight[i][2] = eight[i][3] = 0.f;
   }
 
-  // A record is worked on as a full one or (tail) as one with `valid` < 16 keys.
+  // A record is worked on as a full one or (last) as one with `valid` < 16 keys.
   constexpr std::false_type full;
-  constexpr std::true_type part;
+  constexpr std::true_type last;
 
   // Logits (before sm_scale, times 2^-85) of a record's 16 keys: x[0..1] key g, x[2..3] key
   // g + 8, heads 2 c and 2 c + 1; the keys from `valid` on -> -inf.
@@ -386,7 +390,7 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
         for (int i = 0; i < NREC; ++i) record(full, krec + i * REC, vrec + i * REC, 16);
       } else {
 #pragma unroll 1
-        for (int i = 0; i * 16 < left; ++i) record(part, krec + i * REC, vrec + i * REC, left - i * 16);
+        for (int i = 0; i * 16 < left; ++i) record(last, krec + i * REC, vrec + i * REC, left - i * 16);
       }
       if (p.tile_state && lane == 0)
         p.tile_state[((size_t)b * p.Hkv + kvh) * p.n_k_max + j0 + u * UNIT / kPgTile] = 1;
@@ -438,7 +442,7 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
             for (int i = 0; i < NREC; ++i) record(full, i);
           } else {
 #pragma unroll 1
-            for (int i = 0; i * 16 < left; ++i) record(part, i);
+            for (int i = 0; i * 16 < left; ++i) record(last, i);
           }
           __syncwarp();  // every lane is past its reads of the slot
           vpage = page;
@@ -515,7 +519,7 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
             for (int i = 0; i < NREC; ++i) record(full, i);
           } else {
 #pragma unroll 1
-            for (int i = 0; i * 16 < left; ++i) record(part, i);
+            for (int i = 0; i * 16 < left; ++i) record(last, i);
           }
           __syncwarp();
         }
@@ -536,7 +540,13 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
   }
 
   __syncthreads();  // every warp is past its last use of the slots
-  if (*abort_flag) return;
+  if (*abort_flag) {
+    if (p.clustered) {
+      if (tid < 8) part->lse[tid] = -INFINITY;
+      paged_cluster_merge<D>(p, part, head0, tid, kP4Threads);
+    }
+    return;
+  }
 
   // ---- merge the warps; write the split.
   auto sum_keys = [&](float x) {
@@ -554,7 +564,7 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
   }
   paged_merge_warps<D, W>(
       p, reinterpret_cast<float*>(smem), reinterpret_cast<float2*>(smem + C::kStat), head0, split,
-      tid, m, l, [&](int mt, int i) {
+      tid, m, l, part, [&](int mt, int i) {
         // 2^133 in two steps; the odd rows' codes came 16 times too large
         const float o = acc[mt][i] * kP4PerUnit * ((i >> 1) ? kP4Up / 16.f : kP4Up);
         return PagedCell{(mt >> 1) * 32 + 4 * g + 2 * (mt & 1) + (i >> 1),
@@ -564,6 +574,7 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
     atomicAdd(&p.counts[0], (unsigned long long)n_skipped);
     if (tid == 0) atomicAdd(&p.counts[1], (unsigned long long)ntiles);
   }
+  if (p.clustered) paged_cluster_merge<D>(p, part, head0, tid, kP4Threads);
 }
 
 }  // namespace sskip

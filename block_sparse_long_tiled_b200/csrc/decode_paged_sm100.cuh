@@ -40,6 +40,7 @@ struct PagedDecodeParams {
   unsigned long long* counts;  // {skipped, visited} or null
   uint8_t* tile_state;         // [B, Hkv, n_k_max] or null
   int B, Hq, Hkv, G, S, n_k_max;
+  int clustered;               // the S splits of a head are one cluster, which merges them
   float scale_log2, tsf;
 };
 
@@ -47,6 +48,13 @@ constexpr int kPgTile = 64;
 constexpr int kPgWarps = 4;                          // consumer warps
 constexpr int kPgThreads = (kPgWarps + 1) * 32;
 constexpr int kPgLag = 2;                            // P.V runs this many tiles behind the vote
+
+// A split's result for the merge over its cluster: lse and the normalised O of
+// its heads, in shared memory that nothing else uses any more.
+template <int D>
+struct PagedPart {
+  float lse[8], o[8][D];
+};
 
 template <int D>
 struct PagedCfg {
@@ -61,7 +69,8 @@ struct PagedCfg {
   static constexpr int kBar = kIds + kStages * 16;
   static constexpr int kTotal = kBar + 4 * kStages * 8 + 16;
   static constexpr int kAlloc = kTotal + 1024;                  // the ring starts 1024-aligned
-  static_assert(kPgWarps * 8 * (D + 4) * 4 <= kMax, "the merge of the warps fits the rings");
+  static constexpr int kPart = kPgWarps * 8 * (D + 4) * 4;      // behind the merge of the warps
+  static_assert(kPart + (int)sizeof(PagedPart<D>) <= kMax, "both merges fit the rings");
   static_assert(kStages > kPgLag, "a V slot is free again when its next tile is voted on");
 };
 
@@ -91,14 +100,51 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The splits of a head merged by the cluster they are, each CTA writing its
+// share of the columns: one launch and no trip through memory where a call is
+// short.  All threads of all its CTAs call, also of those whose split was empty
+// or gave up (they left lse = -inf).
+template <int D>
+__device__ __forceinline__ void paged_cluster_merge(const PagedDecodeParams& p,
+                                                    const PagedPart<D>* part, size_t head0, int tid,
+                                                    int threads) {
+  __syncwarp();
+  cluster_sync();  // every CTA's part is written
+  const uint32_t lse0 = smem_u32(part->lse), o0 = smem_u32(part->o);
+  for (int i = (int)cluster_rank() * threads + tid; i < p.G * D; i += p.S * threads) {
+    const int h = i / D;
+    float l[8], mx = -INFINITY;
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      l[s] = s < p.S ? ld_cluster(lse0 + h * 4, s) : -INFINITY;
+      mx = fmaxf(mx, l[s]);
+    }
+    float sum = 0.f, o = 0.f;
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      if (s >= p.S || l[s] == -INFINITY) continue;  // an empty split left no O
+      const float w = __expf(l[s] - mx);
+      sum += w;
+      o = fmaf(w, ld_cluster(o0 + i * 4, s), o);
+    }
+    // Every split empty (a sequence of length 0): O = 0 and lse = -inf.
+    p.o[head0 * D + i] = __float2bfloat16_rn(sum == 0.f ? 0.f : o / sum);
+    if (i % D == 0) p.lse[head0 + h] = mx == -INFINITY ? -INFINITY : mx + __logf(sum);
+  }
+  __syncwarp();
+  cluster_sync();  // no CTA leaves while another may read its shared memory
+}
+
 // What a split without tiles leaves: nothing for the merge to weigh, or (with
 // one split) the empty sequence's O = 0 and lse = -inf.
 template <int D>
-__device__ __forceinline__ void paged_empty_split(const PagedDecodeParams& p, size_t head0,
-                                                  int split, int tid, int threads) {
+__device__ __forceinline__ void paged_empty_split(const PagedDecodeParams& p, PagedPart<D>* part,
+                                                  size_t head0, int split, int tid, int threads) {
   if (p.S == 1) {
     for (int i = tid; i < p.G * D; i += threads) p.o[head0 * D + i] = __float2bfloat16_rn(0.f);
     if (tid < p.G) p.lse[head0 + tid] = -INFINITY;
+  } else if (p.clustered) {
+    if (tid < 8) part->lse[tid] = -INFINITY;
   } else if (tid < p.G) {
     p.lse_part[(head0 + tid) * p.S + split] = -INFINITY;
   }
@@ -152,7 +198,7 @@ template <int D, int W, typename Cell>
 __device__ __forceinline__ void paged_merge_warps(const PagedDecodeParams& p, float* red,
                                                   float2* stat, size_t head0, int split, int tid,
                                                   const float (&m)[2], const float (&l)[2],
-                                                  Cell cell) {
+                                                  PagedPart<D>* part, Cell cell) {
   constexpr int RS = D + 4;  // row stride of the merge buffer: spreads the banks
   const int warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
 #pragma unroll
@@ -187,6 +233,9 @@ __device__ __forceinline__ void paged_merge_warps(const PagedDecodeParams& p, fl
     if (p.S == 1) {
       p.o[(head0 + h) * D + d] = __float2bfloat16_rn(o / sum);
       if (d == 0) p.lse[head0 + h] = lse;
+    } else if (p.clustered) {
+      part->o[h][d] = o / sum;
+      if (d == 0) part->lse[h] = lse;
     } else {
       p.o_part[((head0 + h) * p.S + split) * D + d] = o / sum;
       if (d == 0) p.lse_part[(head0 + h) * p.S + split] = lse;
@@ -220,8 +269,10 @@ __global__ void __launch_bounds__(kPgThreads, PagedCfg<D>::kCtas)
   const int ntiles = max(0, min(n_k, j0 + c_per) - j0);
   const size_t head0 = (size_t)b * p.Hq + (size_t)kvh * p.G;
 
+  auto* part = reinterpret_cast<PagedPart<D>*>(smem + C::kPart);
   if (ntiles == 0) {
-    paged_empty_split<D>(p, head0, split, tid, kPgThreads);
+    paged_empty_split<D>(p, part, head0, split, tid, kPgThreads);
+    if (p.clustered) paged_cluster_merge<D>(p, part, head0, tid, kPgThreads);
     return;
   }
 
@@ -295,6 +346,8 @@ __global__ void __launch_bounds__(kPgThreads, PagedCfg<D>::kCtas)
           if (!SKIP) mbar_wait(vfull(i), ((issued - 1 - i) / NS) & 1, &no_abort);
         }
     }
+    __syncwarp();
+    if (p.clustered) paged_cluster_merge<D>(p, part, head0, tid, kPgThreads);
     return;
   }
 
@@ -516,17 +569,22 @@ __global__ void __launch_bounds__(kPgThreads, PagedCfg<D>::kCtas)
       for (int s = 0; s < NS; ++s)
         if ((v_used >> s) & 1) mbar_wait(vfull(s), ((v_par >> s) & 1) ^ 1, &no_abort);
     }
+    if (p.clustered) {
+      if (tid < 8) part->lse[tid] = -INFINITY;
+      paged_cluster_merge<D>(p, part, head0, tid, kPgThreads);
+    }
     return;
   }
   paged_merge_warps<D, kPgWarps>(p, reinterpret_cast<float*>(smem),
                                  reinterpret_cast<float2*>(smem + C::kStat), head0, split, tid, m,
-                                 l, [&](int mt, int i) {
+                                 l, part, [&](int mt, int i) {
                                    return PagedCell{mt * 16 + g + (i >> 1) * 8, acc[mt][i]};
                                  });
   if (tid == 0 && p.counts) {
     atomicAdd(&p.counts[0], (unsigned long long)n_skipped);
     atomicAdd(&p.counts[1], (unsigned long long)ntiles);
   }
+  if (p.clustered) paged_cluster_merge<D>(p, part, head0, tid, kPgThreads);
 }
 
 // Merge the splits of one (sequence, query head).

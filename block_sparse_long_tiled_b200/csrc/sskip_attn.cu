@@ -833,10 +833,29 @@ bool make_page_map(CUtensorMap* map, const void* base, int d, long long rows, in
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
-int launch_paged_combine(const PagedDecodeParams& p, cudaStream_t st) {
-  if (cudaGetLastError() != cudaSuccess) return SSKIP_ERR_CUDA;
-  if (p.S == 1) return SSKIP_OK;  // the split kernel wrote the result
+// The split kernel, and the merge of the splits where neither the split kernel
+// (one split) nor its clusters did it.
+template <int D, typename... Args>
+int launch_splits(void (*kernel)(Args...), int threads, int smem, const PagedDecodeParams& p,
+                  cudaStream_t st, Args... args) {
+  if (ensure_smem(reinterpret_cast<const void*>(kernel), smem) != cudaSuccess)
+    return SSKIP_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(p.S, p.Hkv, p.B);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = p.S;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = p.clustered ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
+    cudaGetLastError();
+    return SSKIP_ERR_CUDA;
+  }
+  if (p.S == 1 || p.clustered) return SSKIP_OK;
   decode_paged_combine_kernel<D><<<(unsigned)(p.B * p.Hq), 128, 0, st>>>(p);
   return cudaGetLastError() == cudaSuccess ? SSKIP_OK : SSKIP_ERR_CUDA;
 }
@@ -844,22 +863,14 @@ int launch_paged_combine(const PagedDecodeParams& p, cudaStream_t st) {
 template <int D, bool SKIP>
 int launch_decode_paged(const CUtensorMap& mk, const CUtensorMap& mv, const PagedDecodeParams& p,
                         cudaStream_t st) {
-  auto kernel = decode_paged_kernel<D, SKIP>;
-  const int smem = PagedCfg<D>::kAlloc;
-  if (ensure_smem(reinterpret_cast<const void*>(kernel), smem) != cudaSuccess)
-    return SSKIP_ERR_CUDA;
-  kernel<<<dim3(p.S, p.Hkv, p.B), kPgThreads, smem, st>>>(mk, mv, p);
-  return launch_paged_combine<D>(p, st);
+  return launch_splits<D>(decode_paged_kernel<D, SKIP>, kPgThreads, PagedCfg<D>::kAlloc, p, st, mk,
+                          mv, p);
 }
 
 template <int D, bool SKIP>
 int launch_decode_paged4(const PagedDecodeParams& p, cudaStream_t st) {
-  auto kernel = decode_paged4_kernel<D, SKIP>;
-  const int smem = Paged4Cfg<D, SKIP>::kTotal;
-  if (ensure_smem(reinterpret_cast<const void*>(kernel), smem) != cudaSuccess)
-    return SSKIP_ERR_CUDA;
-  kernel<<<dim3(p.S, p.Hkv, p.B), kP4Threads, smem, st>>>(p);
-  return launch_paged_combine<D>(p, st);
+  return launch_splits<D>(decode_paged4_kernel<D, SKIP>, kP4Threads, Paged4Cfg<D, SKIP>::kTotal, p,
+                          st, p);
 }
 
 }  // namespace
@@ -1112,6 +1123,10 @@ SSKIP_API int sskip_attn_decode_paged(const sskip_decode_paged_args* args, void*
   p.n_k_max = (int)(((long long)max_pages * page_size + kPgTile - 1) / kPgTile);
   p.scale_log2 = (float)((double)sm_scale * 1.4426950408889634);
   p.tsf = threshold_scale_factor;
+  // Up to eight splits whose CTAs all run at once merge in their cluster; a
+  // larger call would have the CTAs of short splits wait for long ones while
+  // others queue.
+  p.clustered = num_splits > 1 && num_splits <= 8 && (long long)B * Hkv * num_splits <= 2 * 148;
   if (skip_count && cudaMemsetAsync(skip_count, 0, 2 * sizeof(unsigned long long), st) != cudaSuccess)
     return SSKIP_ERR_CUDA;
   if (tile_state &&

@@ -122,6 +122,7 @@ FMT = pytest.mark.parametrize("fmt", ["bf16", "q4"])
     dict(), dict(d=64), dict(P=16), dict(P=32, d=64), dict(P=128), dict(P=256, d=64),
     dict(Hq=2, Hkv=2), dict(Hq=4, Hkv=2, d=64), dict(Hq=16, Hkv=2), dict(Hq=8, Hkv=1, d=64, P=16),
     dict(splits=1), dict(splits=2), dict(splits=64), dict(splits=1, P=16, d=64),
+    dict(splits=3), dict(splits=5, d=64), dict(splits=7, P=16), dict(splits=8), dict(splits=9),
 ], ids=str)
 def test_ragged_batch(kw, tsf, fmt):
     c = Case([700, 0, 1, 65, 333, 64], fmt=fmt, tsf=tsf, **kw)
