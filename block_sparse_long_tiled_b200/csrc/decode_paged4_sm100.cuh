@@ -417,6 +417,11 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
     uint32_t k_count = 0, v_parity = 0;  // K tiles waited for; phase of V's next wait
     int vkey = 0;  // this lane's first key of the round's tile
     const int rounds = (ntiles + W - 1) / W;
+    // row_passes_log2 without its branches: only (-inf) - (-inf) needs a word.
+    const bool idle[2] = {2 * c >= p.G, 2 * c + 1 >= p.G};  // padding heads always pass
+    auto head_passes = [&](float local, float run, bool idle_head) {
+      return idle_head | (local == -INFINITY) | (local - run < log2_t);
+    };
     for (int r = 0; r <= rounds; ++r, u += W) {
       const bool live = u < units;
       bool keep = false;
@@ -461,6 +466,9 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
               top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], o));
             if (g == 0) wmax[((r & 1) * 8 + 2 * c + h) * W + warp] = top[h] * sl;
           }
+        } else if (g == 0) {
+          wmax[((r & 1) * 8 + 2 * c) * W + warp] = -INFINITY;
+          wmax[((r & 1) * 8 + 2 * c + 1) * W + warp] = -INFINITY;
         }
         named_bar_sync(1, W * 32);  // the maxima of round r are published
         float tw[2][W];
@@ -469,20 +477,15 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
           const float4 v = *reinterpret_cast<const float4*>(&wmax[((r & 1) * 8 + 2 * c + h) * W]);
           tw[h][0] = v.x; tw[h][1] = v.y; tw[h][2] = v.z; tw[h][3] = v.w;
         }
+        // The rule, tile after tile; a dead tile's maxima are -inf and pass.
         const float start[2] = {m[0], m[1]};
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-          if (r * W + i >= ntiles) break;
-          bool pass = true;
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (2 * c + h < p.G) pass = pass && row_passes_log2(tw[h][i], m[h], log2_t, true);
+          const bool pass = head_passes(tw[0][i], m[0], idle[0]) & head_passes(tw[1][i], m[1], idle[1]);
           const bool kept = !__all_sync(0xffffffffu, pass);
-          if (kept) {
-            m[0] = fmaxf(m[0], tw[0][i]);
-            m[1] = fmaxf(m[1], tw[1][i]);
-          }
-          if (i == warp) keep = kept;
+          m[0] = kept ? fmaxf(m[0], tw[0][i]) : m[0];
+          m[1] = kept ? fmaxf(m[1], tw[1][i]) : m[1];
+          keep = i == warp ? kept : keep;
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
