@@ -4,9 +4,13 @@
 // (decode_paged_sm100.cuh); what differs is what bounds it.  A tile is 0.31 of
 // the bytes, so the instructions that widen the codes decide, and the kernel is
 // laid out to spend few others and to keep many warps at it: there is no
-// producer, every warp fetches its own tiles into slots that only it uses, and
-// a warp owns WHOLE units of keys (32 without a threshold, a 64-key tile with
-// one), so that waits, reference checks and votes spread over all of them.
+// producer, every warp owns WHOLE tiles and fetches them itself into a slot
+// that only it uses, so that waits, reference checks and votes spread over 64
+// keys, and the other warps of its sub-partition (three without a threshold,
+// two with one) cover the time a tile takes to arrive.  Measured at 64
+// sequences of 16K-32K (8 kv heads, d = 128, no threshold): half tiles in two
+// slots and 12 warps an SM 448 us, whole tiles in one slot 434, with 16 warps
+// 429.
 //
 // Codes.  A bf16 whose sign and upper seven exponent bits are 0 is its low byte
 // times 2^-133: the subnormals and the first binade are evenly spaced.  So a
@@ -18,9 +22,9 @@
 // values, into the result's rows).  Measured clocks of a sub-partition for one
 // instruction of a warp: logic, shifts, packed bf16 arithmetic 2, the 8x8
 // transpose 4, m16n8k16 bf16 8, m16n8k32 e4m3 24.  The logic pipe is the
-// fullest.  64 sequences of 16K-32K (8 kv heads, d = 128, no threshold), other
-// things equal: 583 us with e4m3 operands, 504 with the codes as 128 + n and a
-// subtraction, 473 with these; 450 with full and last records apart.
+// fullest.  Same workload, other things equal: 583 us with e4m3 operands, 504
+// with the codes as 128 + n and a subtraction, 473 with these, 450 with full
+// and last records apart.
 //
 // Keys: S = sum over groups of sc (q . n) + mn sum(q).  A group's scale multiplies
 // its 32-term product in fp32; the last term is one more product, of the
@@ -49,21 +53,18 @@ constexpr int kP4Threads = kP4Warps * 32;
 
 template <int D, bool SKIP>
 struct Paged4Cfg {
-  static constexpr int kUnit = SKIP ? kPgTile : 32;        // keys a warp takes at a time
-  static constexpr int kBytes = kUnit / 16 * Kv4<D>::kRecord;
-  static constexpr int kSlots = SKIP ? 1 : 3;              // K and V slots of a warp
-  static constexpr int kCtas = 3;                          // per SM
-  static constexpr int kBars = SKIP ? 2 : kSlots;          // of a warp: K and V, or the slots
-  static constexpr int kK = 0;                              // [W][slots]
-  static constexpr int kV = kK + kP4Warps * kSlots * kBytes;
-  static constexpr int kS = kV + kP4Warps * kSlots * kBytes;  // [W][2][64][8] fp32 scores
+  static constexpr int kBytes = 4 * Kv4<D>::kRecord;          // of a tile
+  static constexpr int kCtas = SKIP ? 3 : 4;                  // per SM
+  static constexpr int kK = 0;                                // [W] tiles
+  static constexpr int kV = kK + kP4Warps * kBytes;
+  static constexpr int kS = kV + kP4Warps * kBytes;           // [W][2][64][8] fp32 scores
   static constexpr int kMax = kS + (SKIP ? kP4Warps * 2 * kPgTile * 8 * 4 : 0);  // [2][8][W]
   // The two merges reuse the slots and the scores.
   static constexpr int kPart = kP4Warps * 8 * (D + 4) * 4;
   static constexpr int kMerge = kPart + (int)sizeof(PagedPart<D>);
   static constexpr int kStat = (kMax > kMerge ? kMax : kMerge) + 2 * 8 * kP4Warps * 4;
-  static constexpr int kBar = kStat + kP4Warps * 8 * 8;
-  static constexpr int kTotal = kBar + kP4Warps * kBars * 8 + 16;
+  static constexpr int kBar = kStat + kP4Warps * 8 * 8;       // [W]: a tile's K and V, or K, V apart
+  static constexpr int kTotal = kBar + kP4Warps * 2 * 8 + 16;
 };
 
 constexpr uint32_t kEights = 0x00080008u;              // a pair of 8s, in units of 2^-133
@@ -91,23 +92,24 @@ __device__ __forceinline__ void mma16816_zero(float (&c)[4], uint32_t a0, uint32
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
-// N words of shared memory, aligned to N * 4 bytes (N = 2 or 4).
+// N words at a shared-memory address, aligned to N * 4 bytes (N = 1, 2 or 4).
 template <int N>
-__device__ __forceinline__ void lds_words(uint32_t (&w)[N], const uint8_t* p) {
-  if constexpr (N == 4) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-  } else {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    w[0] = v.x; w[1] = v.y;
-  }
+__device__ __forceinline__ void lds_words(uint32_t (&w)[N], uint32_t addr) {
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(addr));
+  else if constexpr (N == 2)
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+  else
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
 }
 
 template <int D, bool SKIP>
 __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
     decode_paged4_kernel(const PagedDecodeParams p) {
   using C = Paged4Cfg<D, SKIP>;
-  constexpr int W = kP4Warps, UNIT = C::kUnit, NREC = UNIT / 16;
+  constexpr int W = kP4Warps, UNIT = kPgTile, NREC = UNIT / 16;
   constexpr int NG = D / 32;   // groups of a row
   constexpr int MT = D / 16;   // 16-row tiles of O^T
   constexpr int REC = Kv4<D>::kRecord, CODES = Kv4<D>::kCodes;
@@ -135,34 +137,34 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
   }
   const int key0 = j0 * kPgTile;                              // of the split
   const int keys = min(Lb, (j0 + ntiles) * kPgTile) - key0;
-  const int units = (keys + UNIT - 1) / UNIT;
 
-  const uint32_t bars = smem_u32(smem + C::kBar) + warp * C::kBars * 8;  // this warp's
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kBar + W * C::kBars * 8);
-  uint8_t* kbuf = smem + C::kK + warp * C::kSlots * C::kBytes;
-  uint8_t* vbuf = smem + C::kV + warp * C::kSlots * C::kBytes;
+  const uint32_t bars = smem_u32(smem + C::kBar) + warp * 2 * 8;  // this warp's
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kBar + W * 2 * 8);
+  // Shared-memory addresses (32 bits: the loads' arithmetic stays short).
+  const uint32_t kbuf = smem_u32(smem + C::kK) + warp * C::kBytes;
+  const uint32_t vbuf = smem_u32(smem + C::kV) + warp * C::kBytes;
   if (lane == 0) {
-#pragma unroll
-    for (int i = 0; i < C::kBars; ++i) mbar_init(bars + i * 8, 1);
+    mbar_init(bars, 1);
+    mbar_init(bars + 8, 1);
     if (warp == 0) *abort_flag = 0;
     fence_mbar_init();
   }
   __syncthreads();
 
-  // ---- the copies of a unit: one when a page holds it, else UNIT / P, of which
+  // ---- the copies of a tile: one when a page holds it, else 64 / P, of which
   // those behind the last key are not fetched.  Every copy is one lane's (lanes
   // 0 .. 3 K, lanes 4 .. 7 V), which follows its own first key through the split
   // and looks a copy's page up well before it issues the copy.
   const int* table = p.c.block_table + (size_t)b * p.c.max_pages;
-  const int shift = p.c.page_shift, row_shift = min(shift, SKIP ? 6 : 5), rows = 1 << row_shift;
+  const int shift = p.c.page_shift, row_shift = min(shift, 6), rows = 1 << row_shift;
   const int sub = lane & 3, end = key0 + keys;
   const uint32_t copy_bytes = (uint32_t)(rows >> 4) * REC;
   const bool copies = lane < 8 && sub < (UNIT >> row_shift);
   const uint8_t* pool = ((lane & 4) ? p.c.v_pages : p.c.k_pages) +
                         ((size_t)kvh << shift) * (REC / 16);
   const uint32_t page_bytes = (uint32_t)(p.Hkv << shift) * (REC / 16);
-  const uint32_t dst = smem_u32((lane & 4) ? vbuf : kbuf) + sub * copy_bytes;
-  auto page_at = [&](int key) {  // key: this lane's first key of a unit
+  const uint32_t dst = ((lane & 4) ? vbuf : kbuf) + sub * copy_bytes;
+  auto page_at = [&](int key) {  // key: this lane's first key of a tile
     int page = copies && key < end ? __ldg(table + (key >> shift)) : 0;
     if ((uint32_t)page >= (uint32_t)p.c.num_pages) {
       latch_status(kStatusInvalidArg);  // read as page 0
@@ -170,11 +172,11 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
     }
     return page;
   };
-  // The unit whose first key (of lane sub = 0) is k0, this lane's being `key`.
+  // The tile whose first key (of lane sub = 0) is k0, this lane's being `key`.
   // which: bit 0 K, bit 1 V.  Called by the whole warp, on a slot whose last
   // copies have arrived.
-  auto fetch = [&](int k0, int key, int page, int which, int slot, uint32_t bar) {
-    const bool ok = dev_check(k0 < end && slot < C::kSlots);
+  auto fetch = [&](int k0, int key, int page, int which, uint32_t bar) {
+    const bool ok = dev_check(k0 < end);
     if (lane == 0) {
       const uint32_t n = (uint32_t)min(UNIT, (end - k0 + rows - 1) >> row_shift << row_shift);
       if (ok) mbar_arrive_expect_tx(bar, (n >> 4) * REC * (which == 3 ? 2 : 1));
@@ -182,7 +184,7 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
     }
     __syncwarp();
     if (ok && copies && key < end && ((which >> (lane >> 2)) & 1))
-      bulk_load(dst + slot * C::kBytes,
+      bulk_load(dst,
                 pool + (size_t)page * page_bytes +
                     (uint32_t)(key & ((1 << shift) - 1)) * (uint32_t)(REC / 16),
                 copy_bytes, bar);
@@ -193,27 +195,24 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
   };
 
-  int u = warp;  // this warp's next unit to compute
+  int u = warp;  // this warp's next tile of the split
   constexpr int STEP = W * UNIT;
-  int key = key0 + u * UNIT + sub * rows;  // this lane's first key of the next unit to fetch
-  int page = page_at(key);
-  int next_page = 0;       // SKIP: of the unit after the one `page` belongs to
-  bool k_inflight = false; // SKIP
-  if (SKIP) {
-    if (u < units) {
-      fetch(key0 + u * UNIT, key, page, 1, 0, bars);
-      k_inflight = true;
-    }
+  int key = key0 + u * UNIT + sub * rows;  // this lane's first key of the next tile to fetch
+  int page = page_at(key), next_page = 0;  // of that tile and the one after it
+  bool k_inflight = false;                 // K's tile, or the tile
+  if (u < ntiles) {
+    fetch(key0 + u * UNIT, key, page, SKIP ? 1 : 3, bars);
+    k_inflight = true;
     next_page = page_at(key + STEP);
-  } else {
-#pragma unroll
-    for (int i = 0; i < C::kSlots; ++i)
-      if (u + i * W < units) {
-        fetch(key0 + (u + i * W) * UNIT, key, page, 3, i, bars + i * 8);
-        key += STEP;
-        page = page_at(key);
-      }
   }
+  // The next tile into the slot just read.
+  auto fetch_next = [&] {
+    key += STEP;
+    page = next_page;
+    fetch(key0 + (u + W) * UNIT, key, page, SKIP ? 1 : 3, bars);
+    k_inflight = true;
+    next_page = page_at(key + STEP);
+  };
 
   // ---- Q^T of head g: the d's that the key words hold at this lane, times 2^48
   // (even nibbles) or 2^44 (odd ones): a power of two, so still exact.
@@ -260,22 +259,27 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
     eight[i][0] = eight[i][1] = eight[i][2] = eight[i][3] = 0.f;
   }
 
+  // Where this lane's words of a record are.
+  const uint32_t key_at = g * (D / 2) + c * NG * 4, value_at = lane * NG * 4;
+  const uint32_t pair_at = CODES + g * NG * 4, own_at = pair_at + (c % NG) * 4;
+
   // A record is worked on as a full one or (last) as one with `valid` < 16 keys.
   constexpr std::false_type full;
   constexpr std::true_type last;
 
   // Logits (before sm_scale, times 2^-85) of a record's 16 keys: x[0..1] key g, x[2..3] key
   // g + 8, heads 2 c and 2 c + 1; the keys from `valid` on -> -inf.
-  auto scores = [&](auto tail, const uint8_t* rec, int valid, float (&x)[4]) {
+  auto scores = [&](auto tail, uint32_t rec, int valid, float (&x)[4]) {
     uint32_t wa[NG], wb[NG], pa[NG], pb[NG];
-    lds_words<NG>(wa, rec + g * (D / 2) + c * NG * 4);
-    lds_words<NG>(wb, rec + (g + 8) * (D / 2) + c * NG * 4);
-    lds_words<NG>(pa, rec + CODES + g * NG * 4);
-    lds_words<NG>(pb, rec + CODES + (g + 8) * NG * 4);
-    const uint32_t z0 = *reinterpret_cast<const uint32_t*>(rec + CODES + (g * NG + (c % NG)) * 4);
-    const uint32_t z1 = *reinterpret_cast<const uint32_t*>(rec + CODES + ((g + 8) * NG + (c % NG)) * 4);
-    mma16816_zero(x, z0, z1, z0, z1, zf[0], zf[1]);
-    mma16816(x, z0, z1, z0, z1, zf[2], 0u);
+    uint32_t z0[1], z1[1];
+    lds_words<NG>(wa, rec + key_at);
+    lds_words<NG>(wb, rec + key_at + 8 * (D / 2));
+    lds_words<NG>(pa, rec + pair_at);
+    lds_words<NG>(pb, rec + pair_at + 8 * NG * 4);
+    lds_words<1>(z0, rec + own_at);
+    lds_words<1>(z1, rec + own_at + 8 * NG * 4);
+    mma16816_zero(x, z0[0], z1[0], z0[0], z1[0], zf[0], zf[1]);
+    mma16816(x, z0[0], z1[0], z0[0], z1[0], zf[2], 0u);
 #pragma unroll
     for (int gr = 0; gr < NG; ++gr) {
       uint32_t a[4], e[4];
@@ -298,20 +302,20 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
   };
 
   // O^T += V^T P^T over a record's 16 keys.
-  auto accumulate = [&](auto tail, uint8_t* rec, int valid, const float (&pr)[4]) {
+  auto accumulate = [&](auto tail, uint32_t rec, int valid, const float (&pr)[4]) {
     if constexpr (tail.value) {
       // Behind the last key the record holds what an earlier sequence left:
       // its codes are numbers, its scales need not be.  The slot is not
       // fetched into again: this is the sequence's last record.
       for (int i = valid * NG + lane; i < 16 * NG; i += 32)
-        reinterpret_cast<uint32_t*>(rec + CODES)[i] = 0u;
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(rec + CODES + i * 4), "r"(0u) : "memory");
       __syncwarp();
     }
     uint32_t w0[NG], w1[NG], pa[NG], pb[NG];
-    lds_words<NG>(w0, rec + lane * NG * 4);
-    lds_words<NG>(w1, rec + (32 + lane) * NG * 4);
-    lds_words<NG>(pa, rec + CODES + g * NG * 4);
-    lds_words<NG>(pb, rec + CODES + (g + 8) * NG * 4);
+    lds_words<NG>(w0, rec + value_at);
+    lds_words<NG>(w1, rec + value_at + 32 * NG * 4);
+    lds_words<NG>(pa, rec + pair_at);
+    lds_words<NG>(pb, rec + pair_at + 8 * NG * 4);
 #pragma unroll
     for (int gr = 0; gr < NG; ++gr) {
       const float sa = __uint_as_float(pa[gr] << 16), sb = __uint_as_float(pb[gr] << 16);
@@ -351,7 +355,7 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
   int n_skipped = 0;
   if constexpr (!SKIP) {
     float mm[2] = {0.f, 0.f};  // m, or 0 while it is -inf
-    auto record = [&](auto tail, uint8_t* krec, uint8_t* vrec, int valid) {
+    auto record = [&](auto tail, uint32_t krec, uint32_t vrec, int valid) {
       float x[4];
       scores(tail, krec, valid, x);
       // The reference moves only when a score is 2^8 above it: P stays below
@@ -378,35 +382,26 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
       l[1] += pr[1] + pr[3];
       accumulate(tail, vrec, valid, pr);
     };
-    int slot = 0, done = 0;
     uint32_t parity = 0;
-    for (; u < units; u += W, ++done) {
-      if (!await(bars + slot * 8, parity)) break;
-      uint8_t* krec = kbuf + slot * C::kBytes;
-      uint8_t* vrec = vbuf + slot * C::kBytes;
+    for (; u < ntiles; u += W, parity ^= 1) {
+      if (!await(bars, parity)) break;
+      k_inflight = false;
       const int left = keys - u * UNIT;
       if (left >= UNIT) {
 #pragma unroll 1
-        for (int i = 0; i < NREC; ++i) record(full, krec + i * REC, vrec + i * REC, 16);
+        for (int i = 0; i < NREC; ++i) record(full, kbuf + i * REC, vbuf + i * REC, 16);
       } else {
 #pragma unroll 1
-        for (int i = 0; i * 16 < left; ++i) record(last, krec + i * REC, vrec + i * REC, left - i * 16);
+        for (int i = 0; i * 16 < left; ++i) record(last, kbuf + i * REC, vbuf + i * REC, left - i * 16);
       }
       if (p.tile_state && lane == 0)
-        p.tile_state[((size_t)b * p.Hkv + kvh) * p.n_k_max + j0 + u * UNIT / kPgTile] = 1;
+        p.tile_state[((size_t)b * p.Hkv + kvh) * p.n_k_max + j0 + u] = 1;
       __syncwarp();  // every lane is past its reads of the slot
-      if (u + C::kSlots * W < units) {
-        fetch(key0 + (u + C::kSlots * W) * UNIT, key, page, 3, slot, bars + slot * 8);
-        key += STEP;
-        page = page_at(key);
-      }
-      if (++slot == C::kSlots) { slot = 0; parity ^= 1; }
+      if (u + W < ntiles) fetch_next();
     }
-    if (u < units) {  // gave up: wait out this warp's copies before the CTA exits
+    if (k_inflight) {  // gave up: wait out this warp's copies before the CTA exits
       int no_abort = 0;
-      const int issued = min(done + C::kSlots, done + (units - u + W - 1) / W);
-      for (int i = done; i < issued; ++i)
-        mbar_wait(bars + (i % C::kSlots) * 8, (i / C::kSlots) & 1, &no_abort);
+      mbar_wait(bars, parity, &no_abort);
     }
   } else {
     float* wmax = reinterpret_cast<float*>(smem + C::kMax);
@@ -423,7 +418,7 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
       return idle_head | (local == -INFINITY) | (local - run < log2_t);
     };
     for (int r = 0; r <= rounds; ++r, u += W) {
-      const bool live = u < units;
+      const bool live = u < ntiles;
       bool keep = false;
       float a[2] = {1.f, 1.f}, mm[2] = {0.f, 0.f};
       int vpage = 0;
@@ -452,13 +447,7 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
           __syncwarp();  // every lane is past its reads of the slot
           vpage = page;
           vkey = key;
-          if (u + W < units && there) {
-            key += STEP;
-            page = next_page;
-            fetch(key0 + (u + W) * UNIT, key, page, 1, 0, bars);
-            k_inflight = true;
-            next_page = page_at(key + STEP);
-          }
+          if (u + W < ntiles && there) fetch_next();
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -528,7 +517,7 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
         }
       }
       if (keep && !v_inflight) {
-        fetch(key0 + u * UNIT, vkey, vpage, 2, 0, bars + 8);
+        fetch(key0 + u * UNIT, vkey, vpage, 2, bars + 8);
         v_inflight = true;
       }
       kept_prev = keep;
