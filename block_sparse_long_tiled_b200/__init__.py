@@ -804,3 +804,92 @@ def sskip_attn_decode_paged(q, k_pages, v_pages, block_table, seqlens, o, lse, *
         _addr(workspace), ws_bytes, _addr(skip_count), _addr(tile_state), Hq, Hkv, d, num_splits,
         sm_scale, threshold_scale_factor)
     _launch(lib().sskip_attn_decode_paged, args, dev, stream, "sskip_attn_decode_paged")
+
+
+def rope_table(rot_dim: int, base: float, device="cuda", **scaling):
+    """(turns, attn_factor) of sskip_rope_freqs with the table on `device`: what
+    a model keeps for sskip_kv_append."""
+    turns, attn = sskip_rope_freqs(rot_dim, base, **scaling)
+    return torch.from_numpy(turns[:rot_dim // 2]).to(device), attn
+
+
+def paged_cache(num_pages: int, Hkv: int, page_size: int, d: int, *, int4: bool = False,
+                device="cuda"):
+    """Uninitialised (k_pages, v_pages): bf16, or 4-bit records."""
+    if int4:
+        shape, dtype = (num_pages, Hkv, page_size // 16, 10 * d), torch.uint8
+    else:
+        shape, dtype = (num_pages, Hkv, page_size, d), torch.bfloat16
+    if sskip_kv_page_bytes(SSKIP_KV_INT4 if int4 else SSKIP_KV_BF16, Hkv, page_size, d) == 0:
+        raise SSkipError(SSKIP_ERR_UNSUPPORTED, "paged_cache")
+    return tuple(torch.empty(shape, dtype=dtype, device=device) for _ in range(2))
+
+
+def paged_splits(B: int, Hkv: int, max_len: int) -> int:
+    """A num_splits that gives every SM four CTAs where the sequences are long
+    enough (a split has at least four tiles of 64 keys)."""
+    return max(1, min(64, -(-592 // (B * Hkv)), -(-max_len // 256)))
+
+
+def decode_paged(q, k_pages, v_pages, block_table, seqlens, *, sm_scale: float,
+                 threshold_scale_factor: float, num_splits: int | None = None,
+                 with_tiles: bool = False, stream=None) -> dict:
+    """Allocate outputs and workspace with torch and run
+    sskip_attn_decode_paged (num_splits: paged_splits of the table's length)."""
+    B, Hq, d = q.shape
+    Hkv = k_pages.shape[1]
+    cap = block_table.shape[1] * k_pages.shape[2] * (16 if k_pages.dtype == torch.uint8 else 1)
+    S = paged_splits(B, Hkv, cap) if num_splits is None else num_splits
+    with _alloc_on(stream):
+        o = torch.empty_like(q)
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        ws = torch.empty(sskip_attn_decode_workspace_size(B, Hq, d, S), dtype=torch.uint8,
+                         device=q.device)
+        counts = torch.empty(2, dtype=torch.int64, device=q.device)
+        tiles = (torch.empty((B, Hkv, -(-cap // 64)), dtype=torch.uint8, device=q.device)
+                 if with_tiles else None)
+    sskip_attn_decode_paged(q, k_pages, v_pages, block_table, seqlens, o, lse, sm_scale=sm_scale,
+                            threshold_scale_factor=threshold_scale_factor, num_splits=S,
+                            workspace=ws, skip_count=counts, tile_state=tiles, stream=stream)
+    return {"o": o, "lse": lse, "counts": counts, "tile_state": tiles}
+
+
+def prefill_paged(q, k, v, seq_ids, positions, k_pages, v_pages, block_table, *, L: int, turns,
+                  sm_scale: float, threshold_scale_factor: float, interleaved: bool = False,
+                  attn_factor: float = 1.0, q_weight=None, k_weight=None, eps: float = 1e-6,
+                  Br: int = 128, Bc: int = 128, stream=None) -> dict:
+    """A batch of whole prompts of L tokens each, from projections q [B L,Hq,d],
+    k, v [B L,Hkv,d]: append to the paged cache (norm, rotation) and causal
+    prefill of what was appended. Returns prefill's outputs."""
+    T, Hq, d = q.shape
+    Hkv = k.shape[1]
+    with _alloc_on(stream):
+        qr = torch.empty((T // L, Hq, L, d), dtype=q.dtype, device=q.device)
+        kr, vr = (torch.empty((T // L, Hkv, L, d), dtype=q.dtype, device=q.device)
+                  for _ in range(2))
+    sskip_kv_append(q, k, v, seq_ids, positions, q_out=qr, k_out=kr, v_out=vr, k_pages=k_pages,
+                    v_pages=v_pages, block_table=block_table, turns=turns, interleaved=interleaved,
+                    attn_factor=attn_factor, q_weight=q_weight, k_weight=k_weight, eps=eps,
+                    stream=stream)
+    return prefill(qr, kr, vr, causal=True, sm_scale=sm_scale,
+                   threshold_scale_factor=threshold_scale_factor, Br=Br, Bc=Bc, stream=stream)
+
+
+def decode_step_paged(q, k, v, seq_ids, positions, seqlens, k_pages, v_pages, block_table, *,
+                      turns, sm_scale: float, threshold_scale_factor: float,
+                      interleaved: bool = False, attn_factor: float = 1.0, q_weight=None,
+                      k_weight=None, eps: float = 1e-6, num_splits: int | None = None,
+                      stream=None) -> dict:
+    """One decode step of a layer: append the new token of every sequence
+    (q [B,Hq,d], k, v [B,Hkv,d], positions[b] = seqlens[b] - 1) and attend over
+    the cache, the new token included. A padded batch entry has seq_ids[b] < 0
+    and seqlens[b] = 0. Returns decode_paged's outputs."""
+    with _alloc_on(stream):
+        qr = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+    sskip_kv_append(q, k, v, seq_ids, positions, q_out=qr, k_pages=k_pages, v_pages=v_pages,
+                    block_table=block_table, turns=turns, interleaved=interleaved,
+                    attn_factor=attn_factor, q_weight=q_weight, k_weight=k_weight, eps=eps,
+                    stream=stream)
+    return decode_paged(qr, k_pages, v_pages, block_table, seqlens, sm_scale=sm_scale,
+                        threshold_scale_factor=threshold_scale_factor, num_splits=num_splits,
+                        stream=stream)
