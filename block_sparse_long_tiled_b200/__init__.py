@@ -602,6 +602,7 @@ _APPEND_ARGS = struct.Struct(_CACHE + "11P3q7i2f4x")
 _GATHER_ARGS = struct.Struct(_CACHE + "4P4i")
 _DECODE_ARGS = struct.Struct(_CACHE + "5PN2P4i2f")
 _NO_CACHE = (0, 0, 0, 0, 0, 0, 0, 0)
+_BF16, _I32 = torch.bfloat16, torch.int32
 
 
 def _addr(t):
@@ -626,16 +627,12 @@ def _launch(fn, args: bytes, dev: int, stream, what: str) -> None:
 
 def _one_device(*tensors) -> int:
     """The device index that all the given tensors (None: left out) are on."""
-    dev = -1
-    for t in tensors:
-        if t is not None:
-            d = t.get_device()
-            if d < 0:
-                raise ValueError("expected CUDA tensors")
-            if dev < 0:
-                dev = d
-            elif d != dev:
-                raise ValueError(f"tensors on devices {dev} and {d}")
+    devs = {t.get_device() for t in tensors if t is not None}
+    if len(devs) != 1:
+        raise ValueError(f"tensors on several devices: {sorted(devs)}")
+    dev = devs.pop()
+    if dev < 0:
+        raise ValueError("expected CUDA tensors")
     return dev
 
 
@@ -647,19 +644,19 @@ def _pages(k_pages, v_pages, block_table, d):
     if k_pages is None or v_pages is None or block_table is None:
         raise ValueError("a cache needs k_pages, v_pages and block_table")
     shape, dtype = k_pages.shape, k_pages.dtype
-    if v_pages.shape != shape or v_pages.dtype != dtype or len(shape) != 4:
+    if len(shape) != 4 or v_pages.shape != shape or v_pages.dtype is not dtype:
         raise ValueError("k_pages and v_pages must be 4-D and of one shape and dtype")
     if not (k_pages.is_contiguous() and v_pages.is_contiguous() and block_table.is_contiguous()):
         raise ValueError("pages and block table must be contiguous")
-    if block_table.dtype != torch.int32 or block_table.dim() != 2:
+    if block_table.dtype is not _I32 or block_table.dim() != 2:
         raise TypeError("block_table must be a 2-D int32 tensor")
     N, Hkv, rows, width = shape
     B, M = block_table.shape
-    if dtype == torch.uint8:
+    if dtype is torch.uint8:
         if width != 10 * d:
             raise ValueError(f"4-bit records of d = {d} hold {10 * d} bytes, got {width}")
         fmt, rows = SSKIP_KV_INT4, rows * 16
-    elif dtype == torch.bfloat16:
+    elif dtype is _BF16:
         if width != d:
             raise ValueError(f"pages hold rows of {width}, expected d = {d}")
         fmt = SSKIP_KV_BF16
@@ -672,7 +669,7 @@ def _pages(k_pages, v_pages, block_table, d):
 def _token_rows(t, what):
     """[T, H, d] bf16, heads packed, any stride between tokens: that stride (a
     single token's means nothing)."""
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not _BF16:
         raise TypeError(f"{what} must be bf16, got {t.dtype}")
     T, H, d = t.shape
     st, sh, sd = t.stride()
@@ -684,7 +681,7 @@ def _token_rows(t, what):
 def _tokens(t, T, what):
     if t is None:
         return 0
-    if t.dtype != torch.int32 or not t.is_contiguous():
+    if t.dtype is not _I32 or not t.is_contiguous():
         raise TypeError(f"{what} must be contiguous int32")
     if t.numel() != T:
         raise ValueError(f"{what} needs {T} entries")
@@ -693,7 +690,7 @@ def _tokens(t, T, what):
 
 def _rows_out(t, T, H, d, what):
     """out_len of a [T // out_len, H, out_len, d] (or [T, H, d]) output."""
-    if t.dtype != torch.bfloat16 or not t.is_contiguous():
+    if t.dtype is not _BF16 or not t.is_contiguous():
         raise TypeError(f"{what} must be contiguous bf16")
     shape = t.shape
     out_len = 1 if len(shape) == 3 else shape[2]
@@ -705,7 +702,7 @@ def _rows_out(t, T, H, d, what):
 def _weight(t, d, what):
     if t is None:
         return 0
-    if t.dtype != torch.bfloat16 or not t.is_contiguous() or t.numel() != d:
+    if t.dtype is not _BF16 or not t.is_contiguous() or t.numel() != d:
         raise TypeError(f"{what} must be contiguous bf16 of {d} values")
     return t.data_ptr()
 
@@ -737,7 +734,7 @@ def sskip_kv_append(q, k, v, seq_ids, positions, *, q_out=None, k_out=None, v_ou
             out_len = L
     if turns is None:
         rot, turns_at = 0, 0
-    elif turns.dtype != torch.int64 or not turns.is_contiguous():
+    elif turns.dtype is not torch.int64 or not turns.is_contiguous():
         raise TypeError("turns must be contiguous int64")
     else:
         rot, turns_at = 2 * turns.numel(), turns.data_ptr()
@@ -780,13 +777,13 @@ def sskip_attn_decode_paged(q, k_pages, v_pages, block_table, seqlens, o, lse, *
     shape = q.shape
     B, Hq, d = shape
     cache, Hkv = _pages(k_pages, v_pages, block_table, d)
-    if q.dtype != torch.bfloat16 or o.dtype != torch.bfloat16:
+    if q.dtype is not _BF16 or o.dtype is not _BF16:
         raise TypeError("q and o must be bf16")
     if not (q.is_contiguous() and o.is_contiguous() and lse.is_contiguous()):
         raise ValueError("tensors must be contiguous")
     if o.shape != shape or lse.numel() != B * Hq or cache[-1] != B:
         raise ValueError("q, o, lse and block_table must belong to one batch")
-    if lse.dtype != torch.float32:
+    if lse.dtype is not torch.float32:
         raise TypeError(f"lse must be float32, got {lse.dtype}")
     ws_bytes = 0
     if workspace is not None:

@@ -117,6 +117,7 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
   const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+  launch_dependents();  // the merge of the splits waits for all of this kernel
   // seqlens[b] lies in [0, max_pages * P]: another length is latched and
   // clamped, so that no page number is read outside the sequence's table row.
   const int cap = p.c.max_pages << p.c.page_shift;

@@ -256,6 +256,7 @@ __global__ void __launch_bounds__(kPgThreads, PagedCfg<D>::kCtas)
   const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+  launch_dependents();  // the merge of the splits waits for all of this kernel
   // seqlens[b] lies in [0, max_pages * P]: another length is latched and
   // clamped, so that no page number is read outside the sequence's table row.
   const int cap = p.c.max_pages << p.c.page_shift;
@@ -596,6 +597,7 @@ __global__ void __launch_bounds__(128) decode_paged_combine_kernel(const PagedDe
   __shared__ float w_s[64];
   __shared__ float red[4][D];
   __shared__ float sum_s;
+  wait_for_previous_kernel();
   if (warp == 0) {
     const float a = lane < p.S ? lp[lane] : -INFINITY;
     const float e = lane + 32 < p.S ? lp[lane + 32] : -INFINITY;

@@ -856,8 +856,21 @@ int launch_splits(void (*kernel)(Args...), int threads, int smem, const PagedDec
     return SSKIP_ERR_CUDA;
   }
   if (p.S == 1 || p.clustered) return SSKIP_OK;
-  decode_paged_combine_kernel<D><<<(unsigned)(p.B * p.Hq), 128, 0, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? SSKIP_OK : SSKIP_ERR_CUDA;
+  // Started while the splits run, it waits for their end on the device.
+  cudaLaunchConfig_t merge{};
+  merge.gridDim = dim3((unsigned)(p.B * p.Hq));
+  merge.blockDim = dim3(128);
+  merge.stream = st;
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  merge.attrs = &early;
+  merge.numAttrs = 1;
+  if (cudaLaunchKernelEx(&merge, decode_paged_combine_kernel<D>, p) != cudaSuccess) {
+    cudaGetLastError();
+    return SSKIP_ERR_CUDA;
+  }
+  return SSKIP_OK;
 }
 
 template <int D, bool SKIP>
