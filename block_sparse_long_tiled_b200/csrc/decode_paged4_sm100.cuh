@@ -34,7 +34,9 @@
 // Values: O = sum of P' (n - 8) + P (8 sc + mn) with P' = P sc, the group's scale
 // joining P before its rounding to bf16.  The -8 (it halves what that rounding
 // costs) is one more product for each group, of the number 8 with the same
-// rounded P'; the part that does not depend on the code is summed in fp32.
+// rounded P'; the part that does not depend on the code is, for d = 128, one
+// more product, of the record's (sc, mn) pairs with P in bf16 (for d = 64, where
+// a key's pairs do not fill a row of an 8x8 matrix, a sum in fp32).
 //
 // With a threshold the warps take one decision for four tiles at a time: each
 // publishes its tile's maxima, and after one named barrier all walk the four
@@ -92,6 +94,13 @@ __device__ __forceinline__ void mma16816_zero(float (&c)[4], uint32_t a0, uint32
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
+__device__ __forceinline__ void ldsm2_t(uint32_t addr, uint32_t& r0, uint32_t& r1) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];"
+               : "=r"(r0), "=r"(r1)
+               : "r"(addr)
+               : "memory");
+}
+
 // N words at a shared-memory address, aligned to N * 4 bytes (N = 1, 2 or 4).
 template <int N>
 __device__ __forceinline__ void lds_words(uint32_t (&w)[N], uint32_t addr) {
@@ -113,6 +122,7 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
   constexpr int NG = D / 32;   // groups of a row
   constexpr int MT = D / 16;   // 16-row tiles of O^T
   constexpr int REC = Kv4<D>::kRecord, CODES = Kv4<D>::kCodes;
+  constexpr bool ZMMA = NG == 4;  // a key's (sc, mn) pairs are 8 values of 16 bits
   extern __shared__ __align__(1024) uint8_t smem[];
   const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -245,20 +255,21 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
       mine -= __uint_as_float(zf[i] & 0xFFFF0000u);
     }
   }
-  const float sl = p.scale_log2 * kP4PerUnit;
+  const float sl = p.scale_log2 * kP4PerUnit, per_sl = kP4Unit / p.scale_log2;
   const float log2_t = SKIP ? (float)log2((double)p.tsf / (double)Lb) : -INFINITY;
 
   float acc[MT][4];                // O^T of the codes, in units of 2^-133
   float eight[NG][4];              // 8 sum of P', in the same units, the same in every row
-  float zacc[NG][2];               // sum of p (8 sc + mn)
+  // Sum of p (8 sc + mn), or (ZMMA) of p sc and p mn: rows 2 g' and 2 g' + 1 of
+  // a product's result, the other eight rows not used.
+  float zacc[ZMMA ? 2 : NG][2];
   float l[2] = {0.f, 0.f};         // heads 2 c, 2 c + 1
 #pragma unroll
   for (int i = 0; i < MT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
 #pragma unroll
-  for (int i = 0; i < NG; ++i) {
-    zacc[i][0] = zacc[i][1] = 0.f;
-    eight[i][0] = eight[i][1] = eight[i][2] = eight[i][3] = 0.f;
-  }
+  for (int i = 0; i < (ZMMA ? 2 : NG); ++i) zacc[i][0] = zacc[i][1] = 0.f;
+#pragma unroll
+  for (int i = 0; i < NG; ++i) eight[i][0] = eight[i][1] = eight[i][2] = eight[i][3] = 0.f;
 
   // Where this lane's words of a record are.
   const uint32_t key_at = g * (D / 2) + c * NG * 4, value_at = lane * NG * 4;
@@ -317,13 +328,23 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
     lds_words<NG>(w1, rec + value_at + 32 * NG * 4);
     lds_words<NG>(pa, rec + pair_at);
     lds_words<NG>(pb, rec + pair_at + 8 * NG * 4);
+    if constexpr (ZMMA) {
+      uint32_t t0, t1;
+      ldsm2_t(rec + CODES + (lane & 15) * 16, t0, t1);
+      float z[4] = {zacc[0][0], zacc[0][1], zacc[1][0], zacc[1][1]};
+      mma16816(z, t0, 0u, t1, 0u, transpose8x8(pack_bf16x2(pr[0], pr[1])),
+               transpose8x8(pack_bf16x2(pr[2], pr[3])));
+      zacc[0][0] = z[0]; zacc[0][1] = z[1]; zacc[1][0] = z[2]; zacc[1][1] = z[3];
+    }
 #pragma unroll
     for (int gr = 0; gr < NG; ++gr) {
       const float sa = __uint_as_float(pa[gr] << 16), sb = __uint_as_float(pb[gr] << 16);
-      const float za = fmaf(8.f, sa, __uint_as_float(pa[gr] & 0xFFFF0000u));
-      const float zb = fmaf(8.f, sb, __uint_as_float(pb[gr] & 0xFFFF0000u));
-      zacc[gr][0] = fmaf(pr[0], za, fmaf(pr[2], zb, zacc[gr][0]));
-      zacc[gr][1] = fmaf(pr[1], za, fmaf(pr[3], zb, zacc[gr][1]));
+      if constexpr (!ZMMA) {
+        const float za = fmaf(8.f, sa, __uint_as_float(pa[gr] & 0xFFFF0000u));
+        const float zb = fmaf(8.f, sb, __uint_as_float(pb[gr] & 0xFFFF0000u));
+        zacc[gr][0] = fmaf(pr[0], za, fmaf(pr[2], zb, zacc[gr][0]));
+        zacc[gr][1] = fmaf(pr[1], za, fmaf(pr[3], zb, zacc[gr][1]));
+      }
       // The scale joins P before its rounding to bf16 (2^-8 of the product).
       const uint32_t b0 = transpose8x8(pack_bf16x2(pr[0] * sa, pr[1] * sa));
       const uint32_t b1 = transpose8x8(pack_bf16x2(pr[2] * sb, pr[3] * sb));
@@ -343,8 +364,9 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
         acc[i][0] *= a0; acc[i][1] *= a1; acc[i][2] *= a0; acc[i][3] *= a1;
       }
 #pragma unroll
+      for (int i = 0; i < (ZMMA ? 1 : NG); ++i) { zacc[i][0] *= a0; zacc[i][1] *= a1; }
+#pragma unroll
       for (int i = 0; i < NG; ++i) {
-        zacc[i][0] *= a0; zacc[i][1] *= a1;
         eight[i][0] *= a0; eight[i][1] *= a1; eight[i][2] *= a0; eight[i][3] *= a1;
       }
       l[0] *= a0;
@@ -355,30 +377,33 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
   float m[2] = {-INFINITY, -INFINITY};  // reference of heads 2 c, 2 c + 1, in log2 units
   int n_skipped = 0;
   if constexpr (!SKIP) {
-    float mm[2] = {0.f, 0.f};  // m, or 0 while it is -inf
+    // What follows from m: the score (in units of 1 / sl) that moves it, and the
+    // exponent's offset 48 - m (48 while m is -inf).
+    float move_at[2] = {-INFINITY, -INFINITY}, off[2] = {kP4Log, kP4Log};
     auto record = [&](auto tail, uint32_t krec, uint32_t vrec, int valid) {
       float x[4];
       scores(tail, krec, valid, x);
       // The reference moves only when a score is 2^8 above it: P stays below
       // 2^8 (times 2^48) and most records need no exchange between the lanes.
-      float top[2] = {fmaxf(x[0], x[2]) * sl, fmaxf(x[1], x[3]) * sl};
-      if (__any_sync(0xffffffffu, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f)) {
+      float top[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
+      if (__any_sync(0xffffffffu, (top[0] > move_at[0]) | (top[1] > move_at[1]))) {
         float a[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1)
             top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], o));
-          const float mn = fmaxf(m[h], top[h]);
+          const float mn = fmaxf(m[h], top[h] * sl);
           a[h] = m[h] == mn ? 1.f : (m[h] == -INFINITY ? 0.f : ex2_approx(m[h] - mn));
           m[h] = mn;
-          mm[h] = mn == -INFINITY ? 0.f : mn;
+          move_at[h] = (mn + 8.f) * per_sl;
+          off[h] = mn == -INFINITY ? kP4Log : kP4Log - mn;
         }
         rescale(a[0], a[1]);
       }
       float pr[4];
 #pragma unroll
-      for (int h = 0; h < 4; ++h) pr[h] = ex2_approx(fmaf(x[h], sl, kP4Log - mm[h & 1]));
+      for (int h = 0; h < 4; ++h) pr[h] = ex2_approx(fmaf(x[h], sl, off[h & 1]));
       l[0] += pr[0] + pr[2];
       l[1] += pr[1] + pr[3];
       accumulate(tail, vrec, valid, pr);
@@ -413,11 +438,7 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
     uint32_t k_count = 0, v_parity = 0;  // K tiles waited for; phase of V's next wait
     int vkey = 0;  // this lane's first key of the round's tile
     const int rounds = (ntiles + W - 1) / W;
-    // row_passes_log2 without its branches: only (-inf) - (-inf) needs a word.
     const bool idle[2] = {2 * c >= p.G, 2 * c + 1 >= p.G};  // padding heads always pass
-    auto head_passes = [&](float local, float run, bool idle_head) {
-      return idle_head | (local == -INFINITY) | (local - run < log2_t);
-    };
     for (int r = 0; r <= rounds; ++r, u += W) {
       const bool live = u < ntiles;
       bool keep = false;
@@ -471,7 +492,8 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
         const float start[2] = {m[0], m[1]};
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-          const bool pass = head_passes(tw[0][i], m[0], idle[0]) & head_passes(tw[1][i], m[1], idle[1]);
+          const bool pass = paged_head_passes(tw[0][i], m[0], log2_t, idle[0]) &
+                            paged_head_passes(tw[1][i], m[1], log2_t, idle[1]);
           const bool kept = !__all_sync(0xffffffffu, pass);
           m[0] = kept ? fmaxf(m[0], tw[0][i]) : m[0];
           m[1] = kept ? fmaxf(m[1], tw[1][i]) : m[1];
@@ -495,14 +517,15 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
           v_parity ^= 1;
           const int left = keys - (u - W) * UNIT;
           const float* sb = sbuf + ((r - 1) & 1) * SB + g * 8 + 2 * c;
+          const float off[2] = {kP4Log - m_prev[0], kP4Log - m_prev[1]};
           auto record = [&](auto tail, int i) {
             const float2 x0 = *reinterpret_cast<const float2*>(sb + i * 128);
             const float2 x1 = *reinterpret_cast<const float2*>(sb + i * 128 + 64);
             float pr[4];
-            pr[0] = ex2_approx(fmaf(x0.x, sl, kP4Log - m_prev[0]));
-            pr[1] = ex2_approx(fmaf(x0.y, sl, kP4Log - m_prev[1]));
-            pr[2] = ex2_approx(fmaf(x1.x, sl, kP4Log - m_prev[0]));
-            pr[3] = ex2_approx(fmaf(x1.y, sl, kP4Log - m_prev[1]));
+            pr[0] = ex2_approx(fmaf(x0.x, sl, off[0]));
+            pr[1] = ex2_approx(fmaf(x0.y, sl, off[1]));
+            pr[2] = ex2_approx(fmaf(x1.x, sl, off[0]));
+            pr[3] = ex2_approx(fmaf(x1.y, sl, off[1]));
             l[0] += pr[0] + pr[2];
             l[1] += pr[1] + pr[3];
             accumulate(tail, vbuf + i * REC, left - i * 16, pr);
@@ -547,13 +570,20 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
     for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
   };
+  float z[NG][2];  // what does not come from the codes
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
 #pragma unroll
-    for (int gr = 0; gr < NG; ++gr)
-      zacc[gr][h] = sum_keys(zacc[gr][h]) - eight[gr][h] * kP4PerUnit * kP4Up;
+    for (int gr = 0; gr < NG; ++gr) {
+      if constexpr (ZMMA)
+        z[gr][h] = fmaf(8.f, __shfl_sync(0xffffffffu, zacc[0][h], 8 * gr + c),
+                        __shfl_sync(0xffffffffu, zacc[0][h], 8 * gr + 4 + c));
+      else
+        z[gr][h] = sum_keys(zacc[gr][h]);
+      z[gr][h] -= eight[gr][h] * kP4PerUnit * kP4Up;
+    }
     l[h] = sum_keys(l[h]);
-    m[h] -= kP4Log;  // what l, zacc and the codes' part are relative to
+    m[h] -= kP4Log;  // what l, z and the codes' part are relative to
   }
   paged_merge_warps<D, W>(
       p, reinterpret_cast<float*>(smem), reinterpret_cast<float2*>(smem + C::kStat), head0, split,
@@ -561,7 +591,7 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
         // 2^133 in two steps; the odd rows' codes came 16 times too large
         const float o = acc[mt][i] * kP4PerUnit * ((i >> 1) ? kP4Up / 16.f : kP4Up);
         return PagedCell{(mt >> 1) * 32 + 4 * g + 2 * (mt & 1) + (i >> 1),
-                         o + zacc[mt >> 1][i & 1]};
+                         o + z[mt >> 1][i & 1]};
       });
   if (lane == 0 && p.counts) {
     atomicAdd(&p.counts[0], (unsigned long long)n_skipped);

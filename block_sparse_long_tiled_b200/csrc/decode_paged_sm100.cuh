@@ -185,6 +185,12 @@ __device__ __forceinline__ int paged_checked(const PagedRows& c, int page) {
   return 0;
 }
 
+// row_passes_log2 for a positive threshold, without its branches (only
+// (-inf) - (-inf) needs a word of its own).
+__device__ __forceinline__ bool paged_head_passes(float local, float run, float log2_t, bool idle) {
+  return idle | (local == -INFINITY) | (local - run < log2_t);
+}
+
 struct PagedCell {
   int d;
   float x;
@@ -367,7 +373,7 @@ __global__ void __launch_bounds__(kPgThreads, PagedCfg<D>::kCtas)
       }
   }
   float* wmax = reinterpret_cast<float*>(smem + C::kMax);
-  const bool t_positive = SKIP;
+  const bool idle[2] = {2 * c >= p.G, 2 * c + 1 >= p.G};  // padding heads always pass
   const float log2_t = SKIP ? (float)log2((double)p.tsf / (double)Lb) : -INFINITY;
 
   float acc[MT][4];                 // O^T
@@ -510,7 +516,7 @@ __global__ void __launch_bounds__(kPgThreads, PagedCfg<D>::kCtas)
         for (int i = 0; i < 2; ++i) {
           const float4 w = *reinterpret_cast<const float4*>(&wmax[((t & 1) * 8 + 2 * c + i) * kPgWarps]);
           top[i] = fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w));
-          if (2 * c + i < p.G) pass = pass && row_passes_log2(top[i], m[i], log2_t, t_positive);
+          pass &= paged_head_passes(top[i], m[i], log2_t, idle[i]);
         }
         keep = !__all_sync(0xffffffffu, pass);
         if (keep) {

@@ -1114,6 +1114,8 @@ SSKIP_API int sskip_attn_decode_paged(const sskip_decode_paged_args* args, void*
   if (B > 65535 || Hkv > 65535 || num_splits > 64 || (long long)B * Hq > 0x7FFFFFFFll)
     return SSKIP_ERR_UNSUPPORTED;
   if (G != 1 && G != 2 && G != 4 && G != 8) return SSKIP_ERR_UNSUPPORTED;
+  // The 4-bit kernel's scores are kept 2^-85 times what they stand for.
+  if (kv_format == SSKIP_KV_INT4 && sm_scale > 1e12f) return SSKIP_ERR_UNSUPPORTED;
   if (num_splits > 1 &&
       (!workspace || workspace_bytes < sskip_attn_decode_workspace_size(B, Hq, d, num_splits)))
     return SSKIP_ERR_INVALID_ARG;

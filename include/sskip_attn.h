@@ -542,6 +542,9 @@ int sskip_kv_gather(const sskip_kv_gather_args* args, void* stream);
  *     0 not visited, 1 kept, 2 skipped.
  * P is rounded to bf16 for its product with V, the row sum is not; in the
  * 4-bit form the value's scale joins P before that rounding.
+ * SSKIP_KV_INT4 wants sm_scale <= 1e12 (SSKIP_ERR_UNSUPPORTED), |q| < 2^79 and
+ * scales of values between 2^-41 and 2^71: beyond, results overflow, or values
+ * below about 1e-12 lose precision.
  */
 typedef struct {
     sskip_paged_cache cache;  /* one row of the block table a sequence */

@@ -144,7 +144,7 @@ def decode(lib, **kw):
     (dict(Hq=32), UNSUPPORTED), (dict(S=0), INVALID), (dict(S=65), UNSUPPORTED),
     (dict(scale=0.0), INVALID), (dict(tsf=-1.0), INVALID), (dict(tsf=float("nan")), INVALID),
     (dict(B=0), INVALID), (dict(d=80), UNSUPPORTED), (dict(P=80), UNSUPPORTED),
-    (dict(fmt=7), UNSUPPORTED), (dict(B=70000), UNSUPPORTED),
+    (dict(fmt=7), UNSUPPORTED), (dict(B=70000), UNSUPPORTED), (dict(fmt=1, scale=1e13), UNSUPPORTED),
 ], ids=str)
 def test_decode_refuses(lib, kw, rc):
     assert decode(lib, **kw) == rc
