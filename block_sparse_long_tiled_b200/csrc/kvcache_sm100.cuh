@@ -117,7 +117,7 @@ __device__ __forceinline__ void turn_cos_sin(long long pos, unsigned long long t
 
 // ALONE: a warp has a token to itself (else the CTA has one).
 template <int D, bool Q4, bool ALONE>
-__global__ void __launch_bounds__(ALONE ? kAppendAlone * 32 : kAppendMaxWarps * 32, ALONE ? 8 : 2)
+__global__ void __launch_bounds__(ALONE ? kAppendAlone * 32 : kAppendMaxWarps * 32, ALONE ? 7 : 2)
     kv_append_kernel(const AppendParams p) {
   constexpr int LH = D / 16;       // lanes per head
   constexpr int HW = 32 / LH;      // heads a warp holds at a time

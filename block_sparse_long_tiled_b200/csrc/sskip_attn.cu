@@ -791,8 +791,9 @@ int paged_check(const sskip_paged_cache& c, int Hkv, int d) {
   if (d != 64 && d != 128) return SSKIP_ERR_UNSUPPORTED;
   if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)))
     return SSKIP_ERR_UNSUPPORTED;
-  // Positions of a sequence and rows of the cache are 32-bit coordinates.
-  if ((long long)max_pages * page_size > 0x7FFFFFFFll ||
+  // Positions of a sequence and rows of the cache are 32-bit coordinates (the
+  // kernels look a few tiles ahead of a position).
+  if ((long long)max_pages * page_size > (1ll << 30) ||
       (long long)num_pages * Hkv > 0x7FFFFFFFll / page_size)
     return SSKIP_ERR_UNSUPPORTED;
   return SSKIP_OK;
@@ -1027,7 +1028,7 @@ SSKIP_API int sskip_kv_append(const sskip_kv_append_args* args, void* stream) {
   // Up to 16 tokens an SM get a CTA each, of as many warps as the SMs hold at
   // a time (32 query and 8 kv heads, us with 12 / 6 / 4 warps: 148 tokens 3.1 /
   // 3.5 / 3.9, 300 5.0 / 4.1 / 4.4, 600 7.1 / 6.3 / 5.2); more get a warp each
-  // (16K tokens 76 us, 148 with 12 warps, 94 with 4; 1500 tokens 11.8 against
+  // (16K tokens 75 us, 148 with 12 warps, 94 with 4; 1500 tokens 11.8 against
   // 9.1 with 4).
   const bool alone = T > 16 * 148;
   const int warps = std::min(std::min((units + heads - 1) / heads, kAppendMaxWarps),

@@ -407,8 +407,8 @@ int sskip_permute_rows(const void* src, void* dst, const int32_t* idx, long long
  *               starts the 16-bit unit of values 32 a + 4 g .. 32 a + 4 g + 3,
  *               in nibbles 0 .. 3;
  *       scales: byte 8 d + 4 (r (d / 32) + a) holds sc, then mn, of group a.
- * Supported: d in {64, 128}; max_pages * page_size and num_pages * Hkv *
- * page_size below 2^31.  Indices in device memory are checked by the kernels:
+ * Supported: d in {64, 128}; max_pages * page_size up to 2^30 and num_pages *
+ * Hkv * page_size below 2^31.  Indices in device memory are checked by the kernels:
  * a bad one latches SSKIP_ERR_INVALID_ARG (see sskip_get_status) and nothing
  * outside the pools is touched.
  */

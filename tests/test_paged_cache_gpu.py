@@ -162,6 +162,7 @@ def close(got, y, mag):
 @pytest.mark.parametrize("kw", [
     dict(), dict(d=64), dict(interleaved=True), dict(d=64, interleaved=True),
     dict(rot=0), dict(rot=16), dict(rot=48), dict(rot=64), dict(rot=96, interleaved=True),
+    dict(rot=32), dict(rot=80), dict(rot=112), dict(d=64, rot=16), dict(rot=80, interleaved=True),
     dict(d=64, rot=32), dict(d=64, rot=48), dict(norm=False), dict(attn=1.3),
     dict(Hq=1, Hkv=1), dict(Hq=7, Hkv=7, d=64), dict(Hq=64, Hkv=8), dict(Hq=3, Hkv=1, d=64),
     dict(P=32), dict(P=64), dict(P=128), dict(P=256), dict(outs=False),

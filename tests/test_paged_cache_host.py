@@ -92,7 +92,7 @@ def append(lib, **kw):
     (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID), (dict(attn=float("inf")), INVALID),
     (dict(d=96), UNSUPPORTED), (dict(P=48), UNSUPPORTED), (dict(P=8), UNSUPPORTED),
     (dict(P=512), UNSUPPORTED), (dict(fmt=2), UNSUPPORTED), (dict(M=0), INVALID),
-    (dict(N=0), INVALID), (dict(B=0), INVALID), (dict(M=1 << 26), UNSUPPORTED),
+    (dict(N=0), INVALID), (dict(B=0), INVALID), (dict(M=(1 << 24) + 1), UNSUPPORTED),
     (dict(N=1 << 25), UNSUPPORTED),
     # shared memory between an output and anything else
     (dict(qo=at(0)), INVALID), (dict(ko=at(1, 256)), INVALID), (dict(vo=at(9)), INVALID),
