@@ -2,7 +2,7 @@
 
 Thin Python binding of libsskip_attn.so (C ABI in include/sskip_attn.h). The
 sskip_* functions below only marshal torch tensors into the C calls of the
-same names, and the conveniences after them only allocate outputs and chain
+same names (those of the paged cache through the compiled _binding.so), and the conveniences after them only allocate outputs and chain
 those calls: every step of the computation runs in the library, in its CUDA
 kernels or, for the host-side steps (the calibration's factor selection, the
 Hilbert order and the rotation frequencies), in its C++. There is no CPU fallback; a missing
@@ -18,8 +18,8 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib
 import os
-import struct
 
 import torch
 
@@ -54,8 +54,13 @@ class SSkipError(RuntimeError):
 SSKIP_KV_BF16, SSKIP_KV_INT4 = 0, 1
 ROPE_SCALINGS = ("plain", "linear", "bands", "yarn")
 
+# The paged-cache calls and what marshals them in the compiled binding.
+_PAGED = {"sskip_kv_append": "append", "sskip_kv_gather": "gather",
+          "sskip_attn_decode_paged": "decode"}
+
 _lib = None
 _lib_debug = None
+_binding_module = None
 
 
 def lib() -> ctypes.CDLL:
@@ -125,10 +130,13 @@ def _load(path: str) -> ctypes.CDLL:
     L.sskip_kv_page_bytes.argtypes = [I, I, I, I]
     L.sskip_rope_freqs.restype = I
     L.sskip_rope_freqs.argtypes = [I, D, I, D, D, D, D, P, P]
-    # One packed struct and a stream (see the structs in the header).
-    for f in (L.sskip_kv_append, L.sskip_kv_gather, L.sskip_attn_decode_paged):
+    # A struct of the header and a stream; the compiled binding calls them.
+    L.paged_addresses = {}
+    for name in _PAGED:
+        f = getattr(L, name)
         f.restype = I
         f.argtypes = [ctypes.c_char_p, P]
+        L.paged_addresses[name] = ctypes.cast(f, P).value
     L.sskip_get_status.restype = I
     L.sskip_get_status.argtypes = [P]
     L.sskip_selftest_watchdog.restype = I
@@ -595,116 +603,35 @@ def sskip_rope_freqs(rot_dim: int, base: float, *, scaling: str = "plain", facto
     return turns, attn.value
 
 
-# The argument structs of the header, packed in one step: sskip_paged_cache,
-# then the call's own fields.
-_CACHE = "3P5i4x"
-_APPEND_ARGS = struct.Struct(_CACHE + "11P3q7i2f4x")
-_GATHER_ARGS = struct.Struct(_CACHE + "4P4i")
-_DECODE_ARGS = struct.Struct(_CACHE + "5PN2P4i2f")
-_NO_CACHE = (0, 0, 0, 0, 0, 0, 0, 0)
-_BF16, _I32 = torch.bfloat16, torch.int32
+def _marshal():
+    """The compiled marshalling of the paged-cache calls (csrc/binding.cpp)."""
+    global _binding_module
+    if _binding_module is None:
+        if not os.path.exists(os.path.join(_PKG, "_binding.so")):
+            raise RuntimeError(f"{_PKG}/_binding.so is missing: build it with "
+                               "`python -m block_sparse_long_tiled_b200.build`")
+        _binding_module = importlib.import_module(__name__ + "._binding")
+    return _binding_module
 
 
-def _addr(t):
-    return 0 if t is None else t.data_ptr()
-
-
-def _launch(fn, args: bytes, dev: int, stream, what: str) -> None:
-    """Call fn on `stream` (default: the device's current one) with the
-    tensors' device current for the length of the call."""
+def _paged_call(name: str, t, stream, *args) -> None:
+    """Call the library's sskip_* function `name` through the binding, on
+    `stream` (default: the current one of t's device) with t's device current
+    for the length of the call."""
+    L = lib()
+    address, marshal = L.paged_addresses[name], getattr(_marshal(), _PAGED[name])
+    dev = t.get_device()
     if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev)
+        stream = torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else 0
     elif hasattr(stream, "cuda_stream"):
         stream = stream.cuda_stream
-    if torch._C._cuda_getDevice() == dev:
-        rc = fn(args, int(stream))
+    if dev < 0 or torch._C._cuda_getDevice() == dev:
+        rc = marshal(address, int(stream), dev, *args)
     else:
         with torch.cuda.device(dev):
-            rc = fn(args, int(stream))
+            rc = marshal(address, int(stream), dev, *args)
     if rc != SSKIP_OK:
-        raise SSkipError(rc, what)
-
-
-def _one_device(*tensors) -> int:
-    """The device index that all the given tensors (None: left out) are on."""
-    devs = {t.get_device() for t in tensors if t is not None}
-    if len(devs) != 1:
-        raise ValueError(f"tensors on several devices: {sorted(devs)}")
-    dev = devs.pop()
-    if dev < 0:
-        raise ValueError("expected CUDA tensors")
-    return dev
-
-
-def _pages(k_pages, v_pages, block_table, d):
-    """(k, v, table address, format, num_pages, page_size, max_pages, B) and
-    Hkv of a paged cache: bf16 [num_pages, Hkv, page_size, d] or uint8
-    [num_pages, Hkv, page_size // 16, 10 * d] pages and an int32
-    [B, max_pages] block table."""
-    if k_pages is None or v_pages is None or block_table is None:
-        raise ValueError("a cache needs k_pages, v_pages and block_table")
-    shape, dtype = k_pages.shape, k_pages.dtype
-    if len(shape) != 4 or v_pages.shape != shape or v_pages.dtype is not dtype:
-        raise ValueError("k_pages and v_pages must be 4-D and of one shape and dtype")
-    if not (k_pages.is_contiguous() and v_pages.is_contiguous() and block_table.is_contiguous()):
-        raise ValueError("pages and block table must be contiguous")
-    if block_table.dtype is not _I32 or block_table.dim() != 2:
-        raise TypeError("block_table must be a 2-D int32 tensor")
-    N, Hkv, rows, width = shape
-    B, M = block_table.shape
-    if dtype is torch.uint8:
-        if width != 10 * d:
-            raise ValueError(f"4-bit records of d = {d} hold {10 * d} bytes, got {width}")
-        fmt, rows = SSKIP_KV_INT4, rows * 16
-    elif dtype is _BF16:
-        if width != d:
-            raise ValueError(f"pages hold rows of {width}, expected d = {d}")
-        fmt = SSKIP_KV_BF16
-    else:
-        raise TypeError(f"pages must be bf16, or uint8 records, got {dtype}")
-    return (k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), fmt, N, rows, M,
-            B), Hkv
-
-
-def _token_rows(t, what):
-    """[T, H, d] bf16, heads packed, any stride between tokens: that stride (a
-    single token's means nothing)."""
-    if t.dtype is not _BF16:
-        raise TypeError(f"{what} must be bf16, got {t.dtype}")
-    T, H, d = t.shape
-    st, sh, sd = t.stride()
-    if sd != 1 or (sh != d and H > 1):
-        raise ValueError(f"{what}: the heads of a token must be packed")
-    return H * d if T <= 1 else st
-
-
-def _tokens(t, T, what):
-    if t is None:
-        return 0
-    if t.dtype is not _I32 or not t.is_contiguous():
-        raise TypeError(f"{what} must be contiguous int32")
-    if t.numel() != T:
-        raise ValueError(f"{what} needs {T} entries")
-    return t.data_ptr()
-
-
-def _rows_out(t, T, H, d, what):
-    """out_len of a [T // out_len, H, out_len, d] (or [T, H, d]) output."""
-    if t.dtype is not _BF16 or not t.is_contiguous():
-        raise TypeError(f"{what} must be contiguous bf16")
-    shape = t.shape
-    out_len = 1 if len(shape) == 3 else shape[2]
-    if shape[0] * out_len != T or shape[1] != H or shape[-1] != d or len(shape) not in (3, 4):
-        raise ValueError(f"{what} must be [T / out_len, {H}, out_len, {d}] with T = {T}")
-    return out_len
-
-
-def _weight(t, d, what):
-    if t is None:
-        return 0
-    if t.dtype is not _BF16 or not t.is_contiguous() or t.numel() != d:
-        raise TypeError(f"{what} must be contiguous bf16 of {d} values")
-    return t.data_ptr()
+        raise SSkipError(rc, name)
 
 
 def sskip_kv_append(q, k, v, seq_ids, positions, *, q_out=None, k_out=None, v_out=None,
@@ -714,57 +641,20 @@ def sskip_kv_append(q, k, v, seq_ids, positions, *, q_out=None, k_out=None, v_ou
     """Marshal q [T,Hq,d], k, v [T,Hkv,d] bf16 (q, or k and v, may be None),
     seq_ids and positions [T] int32, the norm weights [d] bf16, the int64
     turns table [rot_dim // 2], outputs [T // out_len, H, out_len, d] (or
-    [T, H, d]) and a paged cache into sskip_kv_append."""
-    dev = _one_device(q, k, v, seq_ids, positions, q_out, k_out, v_out, k_pages, v_pages,
-                      block_table, turns, q_weight, k_weight)
-    T, _, d = (q if q is not None else k).shape
-    Hq = Hkv = qs = ks = vs = 0
-    if q is not None:
-        Hq, qs = q.shape[1], _token_rows(q, "q")
-    if k is not None or v is not None:
-        if k is None or v is None or k.shape != v.shape or k.shape[0] != T or k.shape[2] != d:
-            raise ValueError("q, k and v must have one T and d, k and v one shape")
-        Hkv, ks, vs = k.shape[1], _token_rows(k, "k"), _token_rows(v, "v")
-    out_len = 0
-    for t, H, n in ((q_out, Hq, "q_out"), (k_out, Hkv, "k_out"), (v_out, Hkv, "v_out")):
-        if t is not None:
-            L = _rows_out(t, T, H, d, n)
-            if out_len and L != out_len:
-                raise ValueError("q_out, k_out and v_out must share one layout")
-            out_len = L
-    if turns is None:
-        rot, turns_at = 0, 0
-    elif turns.dtype is not torch.int64 or not turns.is_contiguous():
-        raise TypeError("turns must be contiguous int64")
-    else:
-        rot, turns_at = 2 * turns.numel(), turns.data_ptr()
-    cache = _NO_CACHE
-    if k_pages is not None or v_pages is not None:
-        cache, heads = _pages(k_pages, v_pages, block_table, d)
-        if heads != Hkv:
-            raise ValueError(f"the pages hold {heads} heads, k and v {Hkv}")
-    args = _APPEND_ARGS.pack(
-        *cache, _addr(q), _addr(k), _addr(v), _tokens(seq_ids, T, "seq_ids"),
-        _tokens(positions, T, "positions"), _weight(q_weight, d, "q_weight"),
-        _weight(k_weight, d, "k_weight"), turns_at, _addr(q_out), _addr(k_out), _addr(v_out), qs,
-        ks, vs, T, Hq, Hkv, d, rot, 1 if interleaved else 0, out_len or 1, eps, attn_factor)
-    _launch(lib().sskip_kv_append, args, dev, stream, "sskip_kv_append")
+    [T, H, d]) and a paged cache into sskip_kv_append. The cache: bf16
+    [num_pages, Hkv, page_size, d] or uint8 [num_pages, Hkv, page_size // 16,
+    10 * d] pages and an int32 [B, max_pages] block table."""
+    _paged_call("sskip_kv_append", q if q is not None else k, stream, q, k, v, seq_ids, positions,
+                q_out, k_out, v_out, k_pages, v_pages, block_table, turns, interleaved,
+                attn_factor, q_weight, k_weight, eps)
 
 
 def sskip_kv_gather(k_pages, v_pages, block_table, seq_ids, positions, k_out, v_out, *,
                     stream=None) -> None:
     """Marshal a paged cache, seq_ids and positions [T] int32 and bf16 outputs
     [T // out_len, Hkv, out_len, d] (or [T, Hkv, d]) into sskip_kv_gather."""
-    dev = _one_device(k_pages, v_pages, block_table, seq_ids, positions, k_out, v_out)
-    d, T = k_out.shape[-1], seq_ids.numel()
-    cache, Hkv = _pages(k_pages, v_pages, block_table, d)
-    out_len = _rows_out(k_out, T, Hkv, d, "k_out")
-    if _rows_out(v_out, T, Hkv, d, "v_out") != out_len:
-        raise ValueError("k_out and v_out must share one layout")
-    args = _GATHER_ARGS.pack(*cache, _tokens(seq_ids, T, "seq_ids"),
-                             _tokens(positions, T, "positions"), k_out.data_ptr(),
-                             v_out.data_ptr(), T, Hkv, d, out_len)
-    _launch(lib().sskip_kv_gather, args, dev, stream, "sskip_kv_gather")
+    _paged_call("sskip_kv_gather", k_pages, stream, k_pages, v_pages, block_table, seq_ids,
+                positions, k_out, v_out)
 
 
 def sskip_attn_decode_paged(q, k_pages, v_pages, block_table, seqlens, o, lse, *, sm_scale: float,
@@ -772,35 +662,9 @@ def sskip_attn_decode_paged(q, k_pages, v_pages, block_table, seqlens, o, lse, *
                             skip_count=None, tile_state=None, stream=None) -> None:
     """Marshal q [B,Hq,d] bf16, a paged cache, seqlens [B] int32, o [B,Hq,d]
     bf16, lse [B,Hq] fp32 and a uint8 workspace into sskip_attn_decode_paged."""
-    dev = _one_device(q, k_pages, v_pages, block_table, seqlens, o, lse, workspace, skip_count,
-                      tile_state)
-    shape = q.shape
-    B, Hq, d = shape
-    cache, Hkv = _pages(k_pages, v_pages, block_table, d)
-    if q.dtype is not _BF16 or o.dtype is not _BF16:
-        raise TypeError("q and o must be bf16")
-    if not (q.is_contiguous() and o.is_contiguous() and lse.is_contiguous()):
-        raise ValueError("tensors must be contiguous")
-    if o.shape != shape or lse.numel() != B * Hq or cache[-1] != B:
-        raise ValueError("q, o, lse and block_table must belong to one batch")
-    if lse.dtype is not torch.float32:
-        raise TypeError(f"lse must be float32, got {lse.dtype}")
-    ws_bytes = 0
-    if workspace is not None:
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
-        ws_bytes = workspace.numel() * workspace.element_size()
-    if skip_count is not None:
-        _check_counts(skip_count, 2)
-    if tile_state is not None:
-        _dev(tile_state, torch.uint8, "tile_state")
-        if tile_state.numel() != B * Hkv * (-(-cache[6] * cache[5] // 64)):
-            raise ValueError("tile_state must be [B, Hkv, ceil(max_pages * page_size / 64)]")
-    args = _DECODE_ARGS.pack(
-        *cache, q.data_ptr(), _tokens(seqlens, B, "seqlens"), o.data_ptr(), lse.data_ptr(),
-        _addr(workspace), ws_bytes, _addr(skip_count), _addr(tile_state), Hq, Hkv, d, num_splits,
-        sm_scale, threshold_scale_factor)
-    _launch(lib().sskip_attn_decode_paged, args, dev, stream, "sskip_attn_decode_paged")
+    _paged_call("sskip_attn_decode_paged", q, stream, q, k_pages, v_pages, block_table, seqlens, o,
+                lse, sm_scale, threshold_scale_factor, num_splits, workspace, skip_count,
+                tile_state)
 
 
 def rope_table(rot_dim: int, base: float, device="cuda", **scaling):

@@ -60,14 +60,13 @@ def fill(kind, a):
     return bytes(x)
 
 
-def test_the_binding_packs_the_structs_of_the_header():
-    for kind, packed in ((AppendArgs, sk._APPEND_ARGS), (GatherArgs, sk._GATHER_ARGS),
-                         (DecodeArgs, sk._DECODE_ARGS)):
-        assert ctypes.sizeof(kind) == packed.size, kind
-        # every field at its place: fields filled with 1, 2, 3, ... both ways
-        names = [n for n, _ in Cache._fields_] + [n for n, _ in kind._fields_ if n != "cache"]
-        assert fill(kind, {n: i + 1 for i, n in enumerate(names)}) == \
-            packed.pack(*range(1, len(names) + 1))
+@pytest.mark.parametrize("kind,want", [(AppendArgs, 48 + 11 * 8 + 3 * 8 + 7 * 4 + 2 * 4 + 4),
+                                       (GatherArgs, 48 + 4 * 8 + 4 * 4),
+                                       (DecodeArgs, 48 + 8 * 8 + 4 * 4 + 2 * 4)])
+def test_struct_sizes(kind, want):
+    """What a C compiler makes of the header's structs (3 pointers and 5 ints
+    of the cache padded to 48 bytes, then each call's own fields)."""
+    assert ctypes.sizeof(kind) == want
 
 
 def append(lib, **kw):
@@ -210,41 +209,112 @@ def test_reference_records_are_a_bijection(d, value):
     assert all(np.array_equal(a, b) for a, b in zip(got, (codes, sc, mn)))
 
 
-def test_tensor_checks_of_the_binding():
-    z = torch.zeros
-    bf = torch.bfloat16
-    pages, table = z(4, 2, 16, 64, dtype=bf), z(1, 4, dtype=torch.int32)
-    got, heads = sk._pages(pages, pages.clone(), table, 64)
-    assert (got[3:], heads) == ((0, 4, 16, 4, 1), 2)
-    rec = z(4, 2, 1, 640, dtype=torch.uint8)
-    got, heads = sk._pages(rec, rec.clone(), table, 64)
-    assert (got[3:], heads) == ((1, 4, 16, 4, 1), 2)
-    for a, b, t, d, err in [(pages, pages[:, :1], table, 64, ValueError),
-                            (pages, pages.float(), table, 64, ValueError),
-                            (pages.float(), pages.float(), table, 64, TypeError), (pages, None, table, 64, ValueError),
-                            (pages, pages, table.long(), 64, TypeError),
-                            (pages, pages, table, 128, ValueError), (rec, rec, table, 128, ValueError),
-                            (pages.transpose(1, 2), pages.transpose(1, 2), table, 64, ValueError)]:
-        with pytest.raises(err):
-            sk._pages(a, b, t, d)
-    qkv = z(5, 6 * 64, dtype=bf).unflatten(1, (6, 64))
-    assert sk._token_rows(qkv[:, :4], "q") == 6 * 64
-    assert sk._token_rows(qkv[:1, :4], "q") == 4 * 64
-    for t, err in [(qkv.float(), TypeError), (qkv[:, ::2], ValueError), (qkv[..., ::2], ValueError)]:
-        with pytest.raises(err):
-            sk._token_rows(t, "q")
-    assert sk._rows_out(z(5, 4, 64, dtype=bf), 5, 4, 64, "o") == 1
-    assert sk._rows_out(z(2, 4, 3, 64, dtype=bf), 6, 4, 64, "o") == 3
-    for t, err in [(z(5, 4, 64), TypeError), (z(4, 4, 64, dtype=bf), ValueError),
-                   (z(5, 2, 128, dtype=bf), ValueError), (z(5, 4, 128, dtype=bf)[..., ::2], TypeError)]:
-        with pytest.raises(err):
-            sk._rows_out(t, 5, 4, 64, "o")
-    with pytest.raises(ValueError):  # host tensors
-        sk.sskip_kv_append(qkv[:, :4], None, None, None, z(5, dtype=torch.int32),
-                           q_out=z(5, 4, 64, dtype=bf))
-    with pytest.raises(TypeError):
-        sk._tokens(z(5, dtype=torch.int64), 5, "positions")
-    with pytest.raises(ValueError):
-        sk._tokens(z(4, dtype=torch.int32), 5, "positions")
-    with pytest.raises(ValueError):
-        sk._one_device(None, qkv)
+# ------------------------------------------------------------ the binding
+def bf(*shape):
+    return torch.zeros(*shape, dtype=torch.bfloat16)
+
+
+def ints(*shape):
+    return torch.zeros(*shape, dtype=torch.int32)
+
+
+def append_tensors(**kw):
+    qkv = bf(5, 8, 64)
+    a = dict(q=qkv[:, :4], k=qkv[:, 4:6], v=qkv[:, 6:], seq_ids=ints(5), positions=ints(5),
+             q_out=bf(5, 4, 64), k_out=bf(5, 2, 64), v_out=bf(5, 2, 64), k_pages=bf(3, 2, 16, 64),
+             v_pages=bf(3, 2, 16, 64), block_table=ints(2, 4),
+             turns=torch.zeros(32, dtype=torch.int64), q_weight=bf(64), k_weight=bf(64))
+    a.update(kw)
+    return a
+
+
+HOST = "expected CUDA tensors"
+
+
+@pytest.mark.parametrize("kw,err,words", [
+    (dict(), ValueError, HOST),  # every other check passed
+    (dict(k=None, v=None, k_out=None, v_out=None, k_pages=None, v_pages=None), ValueError, HOST),
+    (dict(q=None, q_out=None), ValueError, HOST),
+    (dict(q=bf(1, 4, 64).expand(1, 4, 64), k=bf(1, 2, 64), v=bf(1, 2, 64), seq_ids=ints(1),
+          positions=ints(1), q_out=bf(1, 4, 64), k_out=None, v_out=None), ValueError, HOST),
+    (dict(k_pages=torch.zeros(3, 2, 1, 640, dtype=torch.uint8),
+          v_pages=torch.zeros(3, 2, 1, 640, dtype=torch.uint8)), ValueError, HOST),
+    (dict(q=torch.zeros(5, 4, 64)), TypeError, "q must be BFloat16"),
+    (dict(q=3), (TypeError, AttributeError), ""),
+    (dict(positions=torch.zeros(5, dtype=torch.int64)), TypeError, "positions must be Int"),
+    (dict(positions=ints(4)), ValueError, "positions needs 5"),
+    (dict(seq_ids=ints(10)[::2]), ValueError, "contiguous"),
+    (dict(q=bf(5, 8, 64)[:, ::2]), ValueError, "packed"),
+    (dict(q=bf(5, 4, 128)[..., ::2]), ValueError, "packed"),
+    (dict(q=bf(20, 64)), ValueError, "must be [T, H, d]"),
+    (dict(k=bf(4, 2, 64), v=bf(4, 2, 64)), ValueError, "one T and d"),
+    (dict(v=bf(5, 1, 64)), ValueError, "one shape"),
+    (dict(v=None), ValueError, "come together"),
+    (dict(q_out=bf(5, 3, 64)), ValueError, "q_out must be"),
+    (dict(q_out=bf(5, 4, 128)[..., ::2]), ValueError, "q_out must be contiguous"),
+    (dict(q_out=torch.zeros(5, 4, 64)), TypeError, "q_out"),
+    (dict(q_out=bf(1, 4, 5, 64)), ValueError, "one layout"),
+    (dict(q_weight=bf(32)), ValueError, "q_weight must hold 64"),
+    (dict(k_weight=torch.zeros(64)), TypeError, "k_weight"),
+    (dict(turns=torch.zeros(32)), TypeError, "turns"),
+    (dict(block_table=None), ValueError, "block_table"),
+    (dict(v_pages=None), ValueError, "block_table"),
+    (dict(block_table=ints(2, 4).long()), TypeError, "block_table"),
+    (dict(block_table=ints(8)), ValueError, "2-D"),
+    (dict(k_pages=bf(3, 3, 16, 64), v_pages=bf(3, 3, 16, 64)), ValueError, "the pages hold 3 heads"),
+    (dict(k_pages=bf(3, 2, 16, 128), v_pages=bf(3, 2, 16, 128)), ValueError, "rows of 128"),
+    (dict(k_pages=torch.zeros(3, 2, 1, 1280, dtype=torch.uint8),
+          v_pages=torch.zeros(3, 2, 1, 1280, dtype=torch.uint8)), ValueError, "hold 640 bytes"),
+    (dict(v_pages=bf(3, 2, 32, 64)), ValueError, "one shape and dtype"),
+    (dict(k_pages=torch.zeros(3, 2, 16, 64), v_pages=torch.zeros(3, 2, 16, 64)), TypeError, "pages"),
+    (dict(k_pages=bf(3, 16, 2, 64).transpose(1, 2), v_pages=bf(3, 16, 2, 64).transpose(1, 2)),
+     ValueError, "contiguous"),
+    (dict(eps="small"), TypeError, ""),
+], ids=lambda x: x if isinstance(x, str) else "")
+def test_append_binding_refuses(lib, kw, err, words):
+    with pytest.raises(err) as e:
+        sk.sskip_kv_append(**append_tensors(**kw))
+    assert words in str(e.value)
+
+
+@pytest.mark.parametrize("kw,err,words", [
+    (dict(), ValueError, HOST),
+    (dict(k_out=bf(1, 2, 5, 64), v_out=bf(1, 2, 5, 64)), ValueError, HOST),
+    (dict(k_out=bf(1, 2, 5, 64)), ValueError, "one layout"),
+    (dict(v_out=bf(5, 2, 128)), ValueError, "v_out must be"),
+    (dict(seq_ids=None), (ValueError, AttributeError), ""),
+    (dict(positions=ints(6)), ValueError, "positions needs 5"),
+    (dict(k_pages=bf(3, 2, 16)), ValueError, "4-D"),
+], ids=lambda x: x if isinstance(x, str) else "")
+def test_gather_binding_refuses(lib, kw, err, words):
+    a = dict(k_pages=bf(3, 2, 16, 64), v_pages=bf(3, 2, 16, 64), block_table=ints(2, 4),
+             seq_ids=ints(5), positions=ints(5), k_out=bf(5, 2, 64), v_out=bf(5, 2, 64))
+    a.update(kw)
+    with pytest.raises(err) as e:
+        sk.sskip_kv_gather(**a)
+    assert words in str(e.value)
+
+
+@pytest.mark.parametrize("kw,err,words", [
+    (dict(), ValueError, HOST),
+    (dict(q=bf(2, 8, 128)[..., ::2]), ValueError, "contiguous"),
+    (dict(q=bf(16, 64)), ValueError, "q must be"),
+    (dict(o=bf(2, 4, 64)), ValueError, "one batch"),
+    (dict(lse=torch.zeros(2, 4)), ValueError, "one batch"),
+    (dict(lse=torch.zeros(2, 8, dtype=torch.float64)), TypeError, "lse must be Float"),
+    (dict(block_table=ints(3, 4)), ValueError, "one batch"),
+    (dict(seqlens=torch.zeros(2, dtype=torch.int64)), TypeError, "seqlens must be Int"),
+    (dict(skip_count=torch.zeros(1, dtype=torch.int64)), ValueError, "2 entries"),
+    (dict(skip_count=ints(2)), TypeError, "skip_count"),
+    (dict(tile_state=torch.zeros(5, dtype=torch.uint8)), ValueError, "tile_state must be"),
+    (dict(workspace=torch.zeros(64, dtype=torch.uint8)[::2]), ValueError, "workspace"),
+    (dict(num_splits=1.5), TypeError, ""),
+], ids=lambda x: x if isinstance(x, str) else "")
+def test_decode_binding_refuses(lib, kw, err, words):
+    a = dict(q=bf(2, 8, 64), k_pages=bf(3, 2, 16, 64), v_pages=bf(3, 2, 16, 64),
+             block_table=ints(2, 4), seqlens=ints(2), o=bf(2, 8, 64), lse=torch.zeros(2, 8),
+             sm_scale=0.1, threshold_scale_factor=0.0, num_splits=1, tile_state=None)
+    a.update(kw)
+    with pytest.raises(err) as e:
+        sk.sskip_attn_decode_paged(**a)
+    assert words in str(e.value)
