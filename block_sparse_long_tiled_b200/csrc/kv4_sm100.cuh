@@ -1,7 +1,8 @@
 // kv4_sm100.cuh -- the 4-bit form of keys and values in the paged cache.
 //
 // 32 neighbouring values of a row share a scale and a minimum, both bf16:
-//   mn = min rounded down, sc = (max - mn) / 15 rounded up, n = rint((x - mn) / sc)
+//   mn = min rounded down, sc = (max - mn) / 15 rounded up (2^-126 at least, or
+//   0), n = rint((x - mn) / sc)
 // clamped to 0 .. 15, and the value read back is sc n + mn.  Rounding mn down
 // and sc up keeps every value inside [mn, mn + 15 sc], so no value is off by
 // more than sc / 2.  Codes are those of the exact quotient: with the bf16 inputs
@@ -37,28 +38,40 @@ struct Kv4 {
   static constexpr int kRecord = kCodes + 16 * kGroups * 4;
 };
 
+// Minimum and maximum that keep a NaN.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 __device__ __forceinline__ void kv4_bounds(const float (&x)[8], float& lo, float& hi) {
-  lo = INFINITY;
-  hi = -INFINITY;
+  lo = hi = x[0];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const bool finite = fabsf(x[e]) <= FLT_MAX;
-    lo = fminf(lo, finite ? x[e] : -INFINITY);
-    hi = fmaxf(hi, finite ? x[e] : INFINITY);
+  for (int e = 1; e < 8; ++e) {
+    lo = min_nan(lo, x[e]);
+    hi = max_nan(hi, x[e]);
   }
 }
 
-// rint(y / sc) for 0 <= y <= about 15 sc, ties to even, as the exact quotient
-// gives it: a reciprocal's estimate (off by one at most, next to a tie), put
-// right by the exact remainder.  One division a group instead of one a value:
-// the reciprocal unit takes 8 clocks of a sub-partition for a warp.
+// rint(y / sc), ties to even, for 0 <= y <= about 15 sc, in the low bits of a
+// float (kCodeBias + code).  The quotient is the correctly rounded one: an
+// estimate by the correctly rounded reciprocal, and one correction by the exact
+// remainder (Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990; scales within 2^23 of the smallest can have a
+// subnormal, so inexact, remainder, and then an ulp is off).  One division a
+// group, not one a value: the reciprocal unit takes 8 clocks of a sub-partition
+// for a warp.
+constexpr uint32_t kCodeBias = 0x4B400000u;  // 1.5 * 2^23: adding it rounds to an integer
 __device__ __forceinline__ uint32_t kv4_code(float y, float sc, float inv) {
-  constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
-  float n = fminf(fmaxf(fmaf(y, inv, kRound) - kRound, 0.f), 15.f);
-  const float rest = fmaf(-n, sc, y), over = fabsf(rest) - 0.5f * sc;
-  const bool odd = (uint32_t)n & 1u;
-  if (over > 0.f || (over == 0.f && odd)) n += rest > 0.f ? 1.f : -1.f;
-  return (uint32_t)fminf(fmaxf(n, 0.f), 15.f);
+  const float q = y * inv;
+  const float exact = fmaf(fmaf(-q, sc, y), inv, q);
+  return __float_as_uint(fminf(exact, 15.f) + __uint_as_float(kCodeBias));
 }
 
 // Store row r of a record.  The D / 16 lanes of a head hold chunks m0 and m1
@@ -79,29 +92,29 @@ __device__ __forceinline__ void kv4_store_row(uint8_t* rec, int r, bool value, b
     // split a multiple of 4) one chunk each of four neighbours.
     const bool quad = apart && split > 2;
     if (!quad) {
-      lo[0] = lo[1] = fminf(lo[0], lo[1]);
-      hi[0] = hi[1] = fmaxf(hi[0], hi[1]);
+      lo[0] = lo[1] = min_nan(lo[0], lo[1]);
+      hi[0] = hi[1] = max_nan(hi[0], hi[1]);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      lo[i] = fminf(lo[i], __shfl_xor_sync(kAll, lo[i], 1));
-      hi[i] = fmaxf(hi[i], __shfl_xor_sync(kAll, hi[i], 1));
+      lo[i] = min_nan(lo[i], __shfl_xor_sync(kAll, lo[i], 1));
+      hi[i] = max_nan(hi[i], __shfl_xor_sync(kAll, hi[i], 1));
       const float l2 = __shfl_xor_sync(kAll, lo[i], 2), h2 = __shfl_xor_sync(kAll, hi[i], 2);
       if (quad) {
-        lo[i] = fminf(lo[i], l2);
-        hi[i] = fmaxf(hi[i], h2);
+        lo[i] = min_nan(lo[i], l2);
+        hi[i] = max_nan(hi[i], h2);
       }
     }
   } else {
     const float clo[2] = {lo[0], lo[1]}, chi[2] = {hi[0], hi[1]};
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      float l = fminf((m0 >> 2) == g ? clo[0] : INFINITY, (m1 >> 2) == g ? clo[1] : INFINITY);
-      float h = fmaxf((m0 >> 2) == g ? chi[0] : -INFINITY, (m1 >> 2) == g ? chi[1] : -INFINITY);
+      float l = min_nan((m0 >> 2) == g ? clo[0] : INFINITY, (m1 >> 2) == g ? clo[1] : INFINITY);
+      float h = max_nan((m0 >> 2) == g ? chi[0] : -INFINITY, (m1 >> 2) == g ? chi[1] : -INFINITY);
 #pragma unroll
       for (int o = LH / 2; o > 0; o >>= 1) {
-        l = fminf(l, __shfl_xor_sync(kAll, l, o));
-        h = fmaxf(h, __shfl_xor_sync(kAll, h, o));
+        l = min_nan(l, __shfl_xor_sync(kAll, l, o));
+        h = max_nan(h, __shfl_xor_sync(kAll, h, o));
       }
       if ((m0 >> 2) == g) { lo[0] = l; hi[0] = h; }
       if ((m1 >> 2) == g) { lo[1] = l; hi[1] = h; }
@@ -112,29 +125,33 @@ __device__ __forceinline__ void kv4_store_row(uint8_t* rec, int r, bool value, b
   for (int i = 0; i < 2; ++i) {
     const int m = i ? m1 : m0;
     const float mn = __bfloat162float(__float2bfloat16_rd(lo[i]));
-    const float sc = __bfloat162float(__float2bfloat16_ru(__fdiv_rn(hi[i] - mn, 15.f)));
+    float sc = __bfloat162float(__float2bfloat16_ru(__fdiv_rn(hi[i] - mn, 15.f)));
+    // A NaN or an infinity in the group, or a spread that does not fit.
     const bool bad = !(sc <= FLT_MAX) || !(fabsf(mn) <= FLT_MAX);
-    const bool flat = bad || sc == 0.f;
-    const float up = sc < 0x1p-100f ? 0x1p64f : 1.f;  // a reciprocal within fp32 for any scale
-    const float scu = sc * up, inv = __frcp_rn(scu);
+    if (sc > 0.f) sc = fmaxf(sc, FLT_MIN);  // its reciprocal stays finite
+    const float inv = sc > 0.f ? __frcp_rn(sc) : 0.f;
     uint32_t n[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      n[e] = flat ? 0u : kv4_code(((i ? x1[e] : x0[e]) - mn) * up, scu, inv);
+    for (int e = 0; e < 8; ++e) n[e] = kv4_code((i ? x1[e] : x0[e]) - mn, sc, inv);
     if ((m & 3) == 0) {
-      uint32_t w = bad ? 0x7FFF7FFFu : pack_bf16x2(sc, mn);
+      const uint32_t w = bad ? 0x7FFF7FFFu : pack_bf16x2(sc, mn);
       *reinterpret_cast<uint32_t*>(rec + Kv4<D>::kCodes + (r * NG + (m >> 2)) * 4) = w;
     }
+    // Codes side by side: the biases add up to a constant.
     if (!value) {
-      uint32_t w = 0;
+      uint32_t w = 0, bias = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w |= n[e] << (4 * ((e >> 1) + (e & 1) * 4));
-      *reinterpret_cast<uint32_t*>(rec + r * (D / 2) + ((m & 3) * NG + (m >> 2)) * 4) = w;
+      for (int e = 0; e < 8; ++e) {
+        w += n[e] << (4 * ((e >> 1) + (e & 1) * 4));
+        bias += kCodeBias << (4 * ((e >> 1) + (e & 1) * 4));
+      }
+      *reinterpret_cast<uint32_t*>(rec + r * (D / 2) + ((m & 3) * NG + (m >> 2)) * 4) = w - bias;
     } else {
 #pragma unroll
       for (int qd = 0; qd < 2; ++qd) {
         const int g = (2 * m + qd) & 7;
-        const uint32_t w = n[4 * qd] | n[4 * qd + 1] << 4 | n[4 * qd + 2] << 8 | n[4 * qd + 3] << 12;
+        // kCodeBias has no low bits: 16 bits of the sum are the codes alone
+        const uint32_t w = n[4 * qd] + (n[4 * qd + 1] << 4) + (n[4 * qd + 2] << 8) + (n[4 * qd + 3] << 12);
         *reinterpret_cast<uint16_t*>(rec + ((r >> 3) * 32 + g * 4 + ((r >> 1) & 3)) * NG * 4 +
                                      (m >> 2) * 4 + (r & 1) * 2) = (uint16_t)w;
       }

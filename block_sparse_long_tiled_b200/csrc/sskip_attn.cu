@@ -1026,13 +1026,16 @@ SSKIP_API int sskip_kv_append(const sskip_kv_append_args* args, void* stream) {
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool q4 = cached && a.cache.kv_format == SSKIP_KV_INT4;
   // Up to 16 tokens an SM get a CTA each, of as many warps as the SMs hold at
-  // a time (32 query and 8 kv heads, us with 12 / 6 / 4 warps: 148 tokens 3.1 /
-  // 3.5 / 3.9, 300 5.0 / 4.1 / 4.4, 600 7.1 / 6.3 / 5.2); more get a warp each
-  // (16K tokens 75 us, 148 with 12 warps, 94 with 4; 1500 tokens 11.8 against
-  // 9.1 with 4).
+  // a time (32 query and 8 kv heads, us with 12 / 6 / 4 / 3 warps: 148 tokens 3.0 /
+  // 3.5 / 4.0 / 4.4, 300 5.1 / 4.2 / 4.5 / 5.0, 600 7.0 / 6.3 / 5.3 / 5.6); six
+  // CTAs of four warps fit an SM, so the next two CTAs an SM have three (1000
+  // tokens 8.1 with four, 6.8 with three; 4-bit 9.8 and 9.1), which loses where
+  // there is a second wave anyway (1500 tokens 9.2 and 9.6).  More tokens get a
+  // warp each (16K tokens 75 us, 148 with 12 warps, 94 with 4).
   const bool alone = T > 16 * 148;
+  const int least = T > 6 * 148 && T <= 8 * 148 ? 3 : 4;
   const int warps = std::min(std::min((units + heads - 1) / heads, kAppendMaxWarps),
-                             std::max(4, 148 * 18 / T));
+                             std::max(least, 148 * 18 / T));
   auto kernel =
       d == 128
           ? (q4 ? (alone ? kv_append_kernel<128, true, true> : kv_append_kernel<128, true, false>)

@@ -394,7 +394,8 @@ int sskip_permute_rows(const void* src, void* dst, const int32_t* idx, long long
  *   SSKIP_KV_BF16  [num_pages, Hkv, page_size, d] bf16.
  *   SSKIP_KV_INT4  [num_pages, Hkv, page_size / 16] records of 8 d + 2 d
  *     bytes, 16 rows each.  32 neighbouring values of a row share
- *       mn = min, rounded down to bf16,   sc = (max - mn) / 15, rounded up to bf16,
+ *       mn = min, rounded down to bf16,   sc = (max - mn) / 15, rounded up to bf16
+ *       (a spread above 0 gives at least 2^-126),
  *       n  = rint((x - mn) / sc), ties to even, clamped to 0 .. 15,
  *     and stand for sc n + mn.  A group that holds a NaN or an infinity reads
  *     back as NaN.  The order of the codes, then of the [16][d / 32] bf16

@@ -90,6 +90,7 @@ def quantise(x):
     y = np.asarray(x, np.float64).reshape(*x.shape[:-1], -1, GROUP)
     mn = bf16_toward(y.min(-1), up=False)
     sc = bf16_toward((y.max(-1) - mn) / 15, up=True)
+    sc = np.where(sc > 0, np.maximum(sc, 2.0 ** -126), sc)
     with np.errstate(divide="ignore", invalid="ignore"):
         n = np.rint((y - mn[..., None]) / sc[..., None])
     n = np.where(sc[..., None] > 0, np.clip(n, 0, 15), 0)

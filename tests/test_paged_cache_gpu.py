@@ -284,6 +284,43 @@ def test_q4_groups_that_are_flat_tiny_or_not_finite():
         assert np.all(np.isnan(got[64:]))
 
 
+@pytest.mark.parametrize("fill", [np.nan, np.inf, -np.inf])
+def test_q4_a_value_that_is_not_finite_spoils_its_group_wherever_it_stands(fill):
+    """One such value at each place of a group; the other groups keep theirs."""
+    c = Case(fmt="q4", counts=(32,), starts=(5,), pad=0, Hq=1, Hkv=2, rot=0, norm=False, outs=False)
+    rows = np.random.default_rng(4).standard_normal((32, 2, 128)).astype(np.float32)
+    for i in range(32):
+        rows[i, i % 2, 32 * (i % 4) + i] = fill
+    c.k_t, c.k = bf16(rows)
+    c.v_t, c.v = bf16(rows)
+    c.run()
+    k, v = (torch.zeros(32, 2, 128, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    sk.sskip_kv_gather(c.k_pages, c.v_pages, i32(c.table), i32(c.seq), i32(c.pos), k, v)
+    bad = ~np.isfinite(c.v.astype(np.float64).reshape(32, 2, 4, 32)).all(-1)
+    assert bad.sum() == 32
+    for t in (k, v):
+        got = host(t).reshape(32, 2, 4, 32)
+        assert np.isnan(got[bad]).all() and np.isfinite(got[~bad]).all()
+
+
+@pytest.mark.parametrize("spread", [2.0 ** -133, 2.0 ** -128, 2.0 ** -123, 2.0 ** -122])
+def test_q4_spreads_about_the_smallest_scale(spread):
+    """A scale is 2^-126 at least: codes, scales and minima as the formula says."""
+    c = Case(fmt="q4", counts=(1,), starts=(0,), pad=0, Hq=1, Hkv=1, rot=0, norm=False, outs=False)
+    rows = (np.random.default_rng(5).uniform(-1, 1, (1, 1, 128)) * spread).astype(np.float32)
+    c.k_t, c.k = bf16(rows)
+    c.v_t, c.v = bf16(rows)
+    c.run()
+    k, v = (torch.zeros(1, 1, 128, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    sk.sskip_kv_gather(c.k_pages, c.v_pages, i32(c.table), i32(c.seq), i32(c.pos), k, v)
+    x = c.v.astype(np.float64)
+    sc = np.repeat(ref.quantise(x)[1], 32, -1)
+    assert sc.min() >= 2.0 ** -126
+    for t in (k, v):  # half a scale, and half a step of bf16 (2^-134 where it is subnormal)
+        got = host(t).astype(np.float64)
+        assert np.all(np.abs(got - x) <= 0.5 * sc + np.maximum(2.0 ** -8 * np.abs(got), 2.0 ** -134) + 2.0 ** -149)
+
+
 @pytest.mark.parametrize("d,P,fmt,out_len", [(128, 16, "bf16", 1), (64, 64, "bf16", 4), (128, 32, "q4", 1),
                                              (64, 16, "q4", 3), (64, 256, "q4", 1)])
 def test_gather_reads_what_stands_there(d, P, fmt, out_len):
