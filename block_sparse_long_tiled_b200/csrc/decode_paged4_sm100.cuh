@@ -59,7 +59,7 @@ struct Paged4Cfg {
   static constexpr int kCtas = SKIP ? 3 : 4;                  // per SM
   static constexpr int kK = 0;                                // [W] tiles
   static constexpr int kV = kK + kP4Warps * kBytes;
-  static constexpr int kS = kV + kP4Warps * kBytes;           // [W][2][64][8] fp32 scores
+  static constexpr int kS = kV + kP4Warps * kBytes;           // [2][W][64][8] fp32 scores
   static constexpr int kMax = kS + (SKIP ? kP4Warps * 2 * kPgTile * 8 * 4 : 0);  // [2][8][W]
   // The two merges reuse the slots and the scores.
   static constexpr int kPart = kP4Warps * 8 * (D + 4) * 4;
@@ -432,126 +432,122 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
   } else {
     float* wmax = reinterpret_cast<float*>(smem + C::kMax);
     constexpr int SB = kPgTile * 8;  // a tile's scores: 64 keys, 8 heads
-    float* sbuf = reinterpret_cast<float*>(smem + C::kS) + warp * 2 * SB;
+    float* sbuf = reinterpret_cast<float*>(smem + C::kS) + g * 8 + 2 * c;
+    const uint32_t vbars = smem_u32(smem + C::kBar) + 8, vbase = smem_u32(smem + C::kV) + warp * REC;
     float m_prev[2] = {0.f, 0.f}, a_prev[2] = {1.f, 1.f};  // of the round before
-    bool kept_prev = false, v_inflight = false;
-    uint32_t k_count = 0, v_parity = 0;  // K tiles waited for; phase of V's next wait
+    bool v_inflight = false;
+    uint32_t k_count = 0;                // K tiles waited for
+    uint32_t kept_prev = 0, v_parity = 0;  // a bit a warp: V fetched; phase of the next wait for it
     int vkey = 0;  // this lane's first key of the round's tile
     const int rounds = (ntiles + W - 1) / W;
     const bool idle[2] = {2 * c >= p.G, 2 * c + 1 >= p.G};  // padding heads always pass
     for (int r = 0; r <= rounds; ++r, u += W) {
       const bool live = u < ntiles;
-      bool keep = false;
-      float a[2] = {1.f, 1.f}, mm[2] = {0.f, 0.f};
+      float top[2] = {-INFINITY, -INFINITY};
       int vpage = 0;
-      if (r < rounds) {
-        if (live) {
-          const bool there = k_inflight && await(bars, k_count & 1);
-          if (there) { k_inflight = false; ++k_count; }
-          const int left = keys - u * UNIT;
-          float* sb = sbuf + (r & 1) * SB + g * 8 + 2 * c;
-          float top[2] = {-INFINITY, -INFINITY};
-          auto record = [&](auto tail, int i) {
-            float x[4];
-            scores(tail, kbuf + i * REC, left - i * 16, x);
-            *reinterpret_cast<float2*>(sb + i * 128) = make_float2(x[0], x[1]);
-            *reinterpret_cast<float2*>(sb + i * 128 + 64) = make_float2(x[2], x[3]);
-            top[0] = fmaxf(top[0], fmaxf(x[0], x[2]));
-            top[1] = fmaxf(top[1], fmaxf(x[1], x[3]));
-          };
-          if (left >= UNIT) {
+      if (live) {
+        const bool there = k_inflight && await(bars, k_count & 1);
+        if (there) { k_inflight = false; ++k_count; }
+        const int left = keys - u * UNIT;
+        float* sb = sbuf + (r & 1) * W * SB + warp * SB;
+        auto record = [&](auto tail, int i) {
+          float x[4];
+          scores(tail, kbuf + i * REC, left - i * 16, x);
+          *reinterpret_cast<float2*>(sb + i * 128) = make_float2(x[0], x[1]);
+          *reinterpret_cast<float2*>(sb + i * 128 + 64) = make_float2(x[2], x[3]);
+          top[0] = fmaxf(top[0], fmaxf(x[0], x[2]));
+          top[1] = fmaxf(top[1], fmaxf(x[1], x[3]));
+        };
+        if (left >= UNIT) {
 #pragma unroll 1
-            for (int i = 0; i < NREC; ++i) record(full, i);
-          } else {
+          for (int i = 0; i < NREC; ++i) record(full, i);
+        } else {
 #pragma unroll 1
-            for (int i = 0; i * 16 < left; ++i) record(last, i);
-          }
-          __syncwarp();  // every lane is past its reads of the slot
-          vpage = page;
-          vkey = key;
-          if (u + W < ntiles && there) fetch_next();
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1)
-              top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], o));
-            if (g == 0) wmax[((r & 1) * 8 + 2 * c + h) * W + warp] = top[h] * sl;
-          }
-        } else if (g == 0) {
-          wmax[((r & 1) * 8 + 2 * c) * W + warp] = -INFINITY;
-          wmax[((r & 1) * 8 + 2 * c + 1) * W + warp] = -INFINITY;
+          for (int i = 0; i * 16 < left; ++i) record(last, i);
         }
-        named_bar_sync(1, W * 32);  // the maxima of round r are published
-        float tw[2][W];
+        __syncwarp();  // every lane is past its reads of the slot
+        vpage = page;
+        vkey = key;
+        if (u + W < ntiles && there) fetch_next();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float4 v = *reinterpret_cast<const float4*>(&wmax[((r & 1) * 8 + 2 * c + h) * W]);
-          tw[h][0] = v.x; tw[h][1] = v.y; tw[h][2] = v.z; tw[h][3] = v.w;
-        }
-        // The rule, tile after tile; a dead tile's maxima are -inf and pass.
-        const float start[2] = {m[0], m[1]};
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-          const bool pass = paged_head_passes(tw[0][i], m[0], log2_t, idle[0]) &
-                            paged_head_passes(tw[1][i], m[1], log2_t, idle[1]);
-          const bool kept = !__all_sync(0xffffffffu, pass);
-          m[0] = kept ? fmaxf(m[0], tw[0][i]) : m[0];
-          m[1] = kept ? fmaxf(m[1], tw[1][i]) : m[1];
-          keep = i == warp ? kept : keep;
-        }
+          for (int o = 4; o < 32; o <<= 1)
+            top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], o));
+      }
+      // The kept tiles of round r - 1, whose V tiles have had these scores'
+      // time to arrive: a record of each for every warp.
+      rescale(a_prev[0], a_prev[1]);
+      const float off[2] = {kP4Log - m_prev[0], kP4Log - m_prev[1]};
+#pragma unroll 1
+      for (uint32_t todo = kept_prev; todo; todo &= todo - 1) {
+        const int i = __ffs(todo) - 1;
+        if (!await(vbars + i * 16, (v_parity >> i) & 1)) break;
+        v_parity ^= 1u << i;
+        if (i == warp) v_inflight = false;
+        const int valid = keys - ((r - 1) * W + i) * UNIT - warp * 16;  // of this warp's record
+        const float* sb = sbuf + ((r - 1) & 1) * W * SB + i * SB + warp * 128;
+        auto record = [&](auto tail) {
+          const float2 x0 = *reinterpret_cast<const float2*>(sb);
+          const float2 x1 = *reinterpret_cast<const float2*>(sb + 64);
+          float pr[4];
+          pr[0] = ex2_approx(fmaf(x0.x, sl, off[0]));
+          pr[1] = ex2_approx(fmaf(x0.y, sl, off[1]));
+          pr[2] = ex2_approx(fmaf(x1.x, sl, off[0]));
+          pr[3] = ex2_approx(fmaf(x1.y, sl, off[1]));
+          l[0] += pr[0] + pr[2];
+          l[1] += pr[1] + pr[3];
+          accumulate(tail, vbase + i * C::kBytes, valid, pr);
+        };
+        if (valid >= 16) record(full);
+        else if (valid > 0) record(last);
+      }
+      if (r == rounds) break;
+      if (g == 0) {
+        wmax[((r & 1) * 8 + 2 * c) * W + warp] = top[0] * sl;  // -inf: no such tile
+        wmax[((r & 1) * 8 + 2 * c + 1) * W + warp] = top[1] * sl;
+      }
+      // The maxima of round r are published, and the V slots of round r - 1 read.
+      named_bar_sync(1, W * 32);
+      float tw[2][W];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          a[h] = start[h] == m[h] ? 1.f : (start[h] == -INFINITY ? 0.f : ex2_approx(start[h] - m[h]));
-          mm[h] = m[h] == -INFINITY ? 0.f : m[h];
-        }
-        if (live) {
-          if (!keep) n_skipped += 1;
-          if (p.tile_state && lane == 0)
-            p.tile_state[((size_t)b * p.Hkv + kvh) * p.n_k_max + j0 + u] = keep ? 1 : 2;
+      for (int h = 0; h < 2; ++h) {
+        const float4 v = *reinterpret_cast<const float4*>(&wmax[((r & 1) * 8 + 2 * c + h) * W]);
+        tw[h][0] = v.x; tw[h][1] = v.y; tw[h][2] = v.z; tw[h][3] = v.w;
+      }
+      // The rule, tile after tile; a dead tile's maxima are -inf and pass.
+      uint32_t kept = 0;
+      const float start[2] = {m[0], m[1]};
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        const bool pass = paged_head_passes(tw[0][i], m[0], log2_t, idle[0]) &
+                          paged_head_passes(tw[1][i], m[1], log2_t, idle[1]);
+        const bool keep = !__all_sync(0xffffffffu, pass);
+        m[0] = keep ? fmaxf(m[0], tw[0][i]) : m[0];
+        m[1] = keep ? fmaxf(m[1], tw[1][i]) : m[1];
+        kept |= keep ? 1u << i : 0u;
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        a_prev[h] = start[h] == m[h] ? 1.f : (start[h] == -INFINITY ? 0.f : ex2_approx(start[h] - m[h]));
+        m_prev[h] = m[h] == -INFINITY ? 0.f : m[h];
+      }
+      if (live) {
+        const bool keep = (kept >> warp) & 1;
+        if (!keep) n_skipped += 1;
+        if (p.tile_state && lane == 0)
+          p.tile_state[((size_t)b * p.Hkv + kvh) * p.n_k_max + j0 + u] = keep ? 1 : 2;
+        if (keep && !v_inflight) {
+          fetch(key0 + u * UNIT, vkey, vpage, 2, bars + 8);
+          v_inflight = true;
         }
       }
-      if (r > 0) {  // round r - 1: its V tile has had this round's scores to arrive
-        rescale(a_prev[0], a_prev[1]);
-        if (kept_prev && v_inflight && await(bars + 8, v_parity)) {
-          v_inflight = false;
-          v_parity ^= 1;
-          const int left = keys - (u - W) * UNIT;
-          const float* sb = sbuf + ((r - 1) & 1) * SB + g * 8 + 2 * c;
-          const float off[2] = {kP4Log - m_prev[0], kP4Log - m_prev[1]};
-          auto record = [&](auto tail, int i) {
-            const float2 x0 = *reinterpret_cast<const float2*>(sb + i * 128);
-            const float2 x1 = *reinterpret_cast<const float2*>(sb + i * 128 + 64);
-            float pr[4];
-            pr[0] = ex2_approx(fmaf(x0.x, sl, off[0]));
-            pr[1] = ex2_approx(fmaf(x0.y, sl, off[1]));
-            pr[2] = ex2_approx(fmaf(x1.x, sl, off[0]));
-            pr[3] = ex2_approx(fmaf(x1.y, sl, off[1]));
-            l[0] += pr[0] + pr[2];
-            l[1] += pr[1] + pr[3];
-            accumulate(tail, vbuf + i * REC, left - i * 16, pr);
-          };
-          if (left >= UNIT) {
-#pragma unroll 1
-            for (int i = 0; i < NREC; ++i) record(full, i);
-          } else {
-#pragma unroll 1
-            for (int i = 0; i * 16 < left; ++i) record(last, i);
-          }
-          __syncwarp();
-        }
-      }
-      if (keep && !v_inflight) {
-        fetch(key0 + u * UNIT, vkey, vpage, 2, bars + 8);
-        v_inflight = true;
-      }
-      kept_prev = keep;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) { a_prev[h] = a[h]; m_prev[h] = mm[h]; }
+      kept_prev = kept;
     }
     {  // a wait gave up: wait out this warp's copies before the CTA exits
       int no_abort = 0;
       if (k_inflight) mbar_wait(bars, k_count & 1, &no_abort);
-      if (v_inflight) mbar_wait(bars + 8, v_parity, &no_abort);
+      if (v_inflight) mbar_wait(bars + 8, (v_parity >> warp) & 1, &no_abort);
     }
   }
 
