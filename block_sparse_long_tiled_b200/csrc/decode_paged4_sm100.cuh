@@ -175,14 +175,9 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
                         ((size_t)kvh << shift) * (REC / 16);
   const uint32_t page_bytes = (uint32_t)(p.Hkv << shift) * (REC / 16);
   const uint32_t dst = ((lane & 4) ? vbuf : kbuf) + sub * copy_bytes;
-  auto page_at = [&](int key) {  // key: this lane's first key of a tile
-    int page = copies && key < end ? __ldg(table + (key >> shift)) : 0;
-    if ((uint32_t)page >= (uint32_t)p.c.num_pages) {
-      latch_status(kStatusInvalidArg);  // read as page 0
-      page = 0;
-    }
-    return page;
-  };
+  // key: this lane's first key of a tile.  Nothing looks at the number before
+  // the copy is issued: the look-up is a trip to memory.
+  auto page_at = [&](int key) { return copies && key < end ? __ldg(table + (key >> shift)) : 0; };
   // The tile whose first key (of lane sub = 0) is k0, this lane's being `key`.
   // which: bit 0 K, bit 1 V.  Called by the whole warp, on a slot whose last
   // copies have arrived.
@@ -194,11 +189,16 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
       else mbar_arrive(bar);  // the phase completes without data
     }
     __syncwarp();
-    if (ok && copies && key < end && ((which >> (lane >> 2)) & 1))
+    if (ok && copies && key < end && ((which >> (lane >> 2)) & 1)) {
+      if ((uint32_t)page >= (uint32_t)p.c.num_pages) {
+        latch_status(kStatusInvalidArg);  // read as page 0
+        page = 0;
+      }
       bulk_load(dst,
                 pool + (size_t)page * page_bytes +
                     (uint32_t)(key & ((1 << shift) - 1)) * (uint32_t)(REC / 16),
                 copy_bytes, bar);
+    }
   };
   // A wait that gives up is the same for the whole warp; what it waited for
   // stays in flight and its slot is not fetched into again.
@@ -259,7 +259,11 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
   const float log2_t = SKIP ? (float)log2((double)p.tsf / (double)Lb) : -INFINITY;
 
   float acc[MT][4];                // O^T of the codes, in units of 2^-133
-  float eight[NG][4];              // 8 sum of P', in the same units, the same in every row
+  // 8 sum of P', in the same units: a group in an accumulator of its own, the
+  // same in every row, or (four groups) group gr in rows 4 gr .. 4 gr + 3 of one,
+  // which saves the registers that made the kernel spill (407 us and 398).
+  constexpr int NE = NG == 4 ? 1 : NG;
+  float eight[NE][4];
   // Sum of p (8 sc + mn), or (ZMMA) of p sc and p mn: rows 2 g' and 2 g' + 1 of
   // a product's result, the other eight rows not used.
   float zacc[ZMMA ? 2 : NG][2];
@@ -269,7 +273,8 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
 #pragma unroll
   for (int i = 0; i < (ZMMA ? 2 : NG); ++i) zacc[i][0] = zacc[i][1] = 0.f;
 #pragma unroll
-  for (int i = 0; i < NG; ++i) eight[i][0] = eight[i][1] = eight[i][2] = eight[i][3] = 0.f;
+  for (int i = 0; i < NE; ++i) eight[i][0] = eight[i][1] = eight[i][2] = eight[i][3] = 0.f;
+  const uint32_t e_lo = lane < 16 ? kEights : 0u, e_hi = lane >= 16 ? kEights : 0u;
 
   // Where this lane's words of a record are.
   const uint32_t key_at = g * (D / 2) + c * NG * 4, value_at = lane * NG * 4;
@@ -353,7 +358,13 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
       widen_codes(w1[gr], e);
       mma16816(acc[2 * gr], a[0], a[1], e[0], e[1], b0, b1);
       mma16816(acc[2 * gr + 1], a[2], a[3], e[2], e[3], b0, b1);
-      mma16816(eight[gr], kEights, kEights, kEights, kEights, b0, b1);
+      if constexpr (NE == 1) {
+        const uint32_t e8 = (gr & 1) ? e_hi : e_lo;
+        if (gr < 2) mma16816(eight[0], e8, 0u, e8, 0u, b0, b1);
+        else mma16816(eight[0], 0u, e8, 0u, e8, b0, b1);
+      } else {
+        mma16816(eight[gr], kEights, kEights, kEights, kEights, b0, b1);
+      }
     }
   };
 
@@ -366,7 +377,7 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
 #pragma unroll
       for (int i = 0; i < (ZMMA ? 1 : NG); ++i) { zacc[i][0] *= a0; zacc[i][1] *= a1; }
 #pragma unroll
-      for (int i = 0; i < NG; ++i) {
+      for (int i = 0; i < NE; ++i) {
         eight[i][0] *= a0; eight[i][1] *= a1; eight[i][2] *= a0; eight[i][3] *= a1;
       }
       l[0] *= a0;
@@ -435,12 +446,13 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
     float* sbuf = reinterpret_cast<float*>(smem + C::kS) + g * 8 + 2 * c;
     const uint32_t vbars = smem_u32(smem + C::kBar) + 8, vbase = smem_u32(smem + C::kV) + warp * REC;
     float m_prev[2] = {0.f, 0.f}, a_prev[2] = {1.f, 1.f};  // of the round before
+    float mw = -INFINITY;  // the running maximum of head lane & 7, which the rule is walked on
     bool v_inflight = false;
     uint32_t k_count = 0;                // K tiles waited for
     uint32_t kept_prev = 0, v_parity = 0;  // a bit a warp: V fetched; phase of the next wait for it
     int vkey = 0;  // this lane's first key of the round's tile
     const int rounds = (ntiles + W - 1) / W;
-    const bool idle[2] = {2 * c >= p.G, 2 * c + 1 >= p.G};  // padding heads always pass
+    const bool idle = (lane & 7) >= p.G;  // padding heads always pass
     for (int r = 0; r <= rounds; ++r, u += W) {
       const bool live = u < ntiles;
       float top[2] = {-INFINITY, -INFINITY};
@@ -509,28 +521,27 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
       }
       // The maxima of round r are published, and the V slots of round r - 1 read.
       named_bar_sync(1, W * 32);
-      float tw[2][W];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float4 v = *reinterpret_cast<const float4*>(&wmax[((r & 1) * 8 + 2 * c + h) * W]);
-        tw[h][0] = v.x; tw[h][1] = v.y; tw[h][2] = v.z; tw[h][3] = v.w;
-      }
-      // The rule, tile after tile; a dead tile's maxima are -inf and pass.
+      // The rule, tile after tile, a head a lane (four lanes the same); a dead
+      // tile's maxima are -inf and pass.
+      const float4 v = *reinterpret_cast<const float4*>(&wmax[((r & 1) * 8 + (lane & 7)) * W]);
+      const float tw[W] = {v.x, v.y, v.z, v.w};
       uint32_t kept = 0;
-      const float start[2] = {m[0], m[1]};
+      const float start = mw;
 #pragma unroll
       for (int i = 0; i < W; ++i) {
-        const bool pass = paged_head_passes(tw[0][i], m[0], log2_t, idle[0]) &
-                          paged_head_passes(tw[1][i], m[1], log2_t, idle[1]);
-        const bool keep = !__all_sync(0xffffffffu, pass);
-        m[0] = keep ? fmaxf(m[0], tw[0][i]) : m[0];
-        m[1] = keep ? fmaxf(m[1], tw[1][i]) : m[1];
+        const bool keep = !__all_sync(0xffffffffu, paged_head_passes(tw[i], mw, log2_t, idle));
+        mw = keep ? fmaxf(mw, tw[i]) : mw;
         kept |= keep ? 1u << i : 0u;
       }
+      a_prev[0] = a_prev[1] = 1.f;
+      if (kept) {
+        const float aw = start == mw ? 1.f : (start == -INFINITY ? 0.f : ex2_approx(start - mw));
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        a_prev[h] = start[h] == m[h] ? 1.f : (start[h] == -INFINITY ? 0.f : ex2_approx(start[h] - m[h]));
-        m_prev[h] = m[h] == -INFINITY ? 0.f : m[h];
+        for (int h = 0; h < 2; ++h) {
+          a_prev[h] = __shfl_sync(0xffffffffu, aw, 2 * c + h);
+          m[h] = __shfl_sync(0xffffffffu, mw, 2 * c + h);
+          m_prev[h] = m[h] == -INFINITY ? 0.f : m[h];
+        }
       }
       if (live) {
         const bool keep = (kept >> warp) & 1;
@@ -576,7 +587,9 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
                         __shfl_sync(0xffffffffu, zacc[0][h], 8 * gr + 4 + c));
       else
         z[gr][h] = sum_keys(zacc[gr][h]);
-      z[gr][h] -= eight[gr][h] * kP4PerUnit * kP4Up;
+      const float e8 = NE == 1 ? __shfl_sync(0xffffffffu, eight[0][(gr >> 1) * 2 + h], (gr & 1) * 16 + c)
+                               : eight[gr % NE][h];
+      z[gr][h] -= e8 * kP4PerUnit * kP4Up;
     }
     l[h] = sum_keys(l[h]);
     m[h] -= kP4Log;  // what l, z and the codes' part are relative to
