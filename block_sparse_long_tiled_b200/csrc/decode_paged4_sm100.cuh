@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
   const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  launch_dependents();  // the merge of the splits waits for all of this kernel
+  start_behind_previous_kernel();
   // seqlens[b] lies in [0, max_pages * P]: another length is latched and
   // clamped, so that no page number is read outside the sequence's table row.
   const int cap = p.c.max_pages << p.c.page_shift;
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
   const uint32_t dst = ((lane & 4) ? vbuf : kbuf) + sub * copy_bytes;
   // key: this lane's first key of a tile.  Nothing looks at the number before
   // the copy is issued: the look-up is a trip to memory.
-  auto page_at = [&](int key) { return copies && key < end ? __ldg(table + (key >> shift)) : 0; };
+  auto page_at = [&](int key) { return copies && key < end ? table[key >> shift] : 0; };
   // The tile whose first key (of lane sub = 0) is k0, this lane's being `key`.
   // which: bit 0 K, bit 1 V.  Called by the whole warp, on a slot whose last
   // copies have arrived.
@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
           top[1] = fmaxf(top[1], fmaxf(x[1], x[3]));
         };
         if (left >= UNIT) {
-#pragma unroll 1
+#pragma unroll 2  // 371 us, 379 one by one, 376 by four
           for (int i = 0; i < NREC; ++i) record(full, i);
         } else {
 #pragma unroll 1

@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kPgThreads, PagedCfg<D>::kCtas)
   const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  launch_dependents();  // the merge of the splits waits for all of this kernel
+  start_behind_previous_kernel();
   // seqlens[b] lies in [0, max_pages * P]: another length is latched and
   // clamped, so that no page number is read outside the sequence's table row.
   const int cap = p.c.max_pages << p.c.page_shift;
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kPgThreads, PagedCfg<D>::kCtas)
     const bool mine = lane < (SKIP ? 8 : 16) && ln.half < D / 64;
     // The page of this lane's copy of a tile, loaded a tile ahead.
     auto page_of = [&](int j) {
-      return mine && j < n_k && ln.sub < ln.copies(j, Lb) ? __ldg(table + ln.slot(j)) : 0;
+      return mine && j < n_k && ln.sub < ln.copies(j, Lb) ? table[ln.slot(j)] : 0;
     };
     int issued = 0, s = 0, par = 1, next = page_of(j0);
     bool ok = true;
@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(128) decode_paged_combine_kernel(const PagedDe
   __shared__ float w_s[64];
   __shared__ float red[4][D];
   __shared__ float sum_s;
-  wait_for_previous_kernel();
+  start_behind_previous_kernel();
   if (warp == 0) {
     const float a = lane < p.S ? lp[lane] : -INFINITY;
     const float e = lane + 32 < p.S ? lp[lane + 32] : -INFINITY;

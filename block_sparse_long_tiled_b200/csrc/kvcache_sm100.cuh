@@ -75,7 +75,7 @@ __device__ __forceinline__ bool locate_row(const PagedRows& c, int seq, int pos,
     latch_status(kStatusInvalidArg);
     return false;
   }
-  *page = __ldg(c.block_table + (size_t)seq * c.max_pages + slot);
+  *page = c.block_table[(size_t)seq * c.max_pages + slot];
   *off = pos & ((1 << c.page_shift) - 1);
   if (*page < 0 || *page >= c.num_pages) {
     latch_status(kStatusInvalidArg);
@@ -85,7 +85,7 @@ __device__ __forceinline__ bool locate_row(const PagedRows& c, int seq, int pos,
 }
 
 __device__ __forceinline__ uint4 load_raw(const __nv_bfloat16* p) {
-  return __ldg(reinterpret_cast<const uint4*>(p));
+  return *reinterpret_cast<const uint4*>(p);
 }
 
 __device__ __forceinline__ void store_chunk(__nv_bfloat16* p, const float (&x)[8]) {
@@ -121,6 +121,7 @@ __global__ void __launch_bounds__(ALONE ? kAppendAlone * 32 : kAppendMaxWarps * 
     kv_append_kernel(const AppendParams p) {
   constexpr int LH = D / 16;       // lanes per head
   constexpr int HW = 32 / LH;      // heads a warp holds at a time
+  start_behind_previous_kernel();
   // cosine and sine of pair 8 j + e at e LH + j
   __shared__ float tabs[ALONE ? kAppendAlone : 1][2][D / 2];
   const int lane = threadIdx.x & 31, j = lane % LH, hs = lane / LH;
@@ -128,8 +129,8 @@ __global__ void __launch_bounds__(ALONE ? kAppendAlone * 32 : kAppendMaxWarps * 
   const int t = ALONE ? blockIdx.x * kAppendAlone + (threadIdx.x >> 5) : blockIdx.x;
   if (ALONE && t >= p.T) return;
   auto& tab = tabs[ALONE ? threadIdx.x >> 5 : 0];
-  const int pos = p.positions ? __ldg(p.positions + t) : 0;
-  const int seq = p.seq_ids ? __ldg(p.seq_ids + t) : 0;
+  const int pos = p.positions ? p.positions[t] : 0;
+  const int seq = p.seq_ids ? p.seq_ids[t] : 0;
   // The lane's pairs 8 j .. 8 j + 7: in chunks (j, j + rot / 16) when pairs are
   // half the rotated part apart, in (2 j, 2 j + 1) when they are neighbours or
   // not rotated at all.
@@ -163,7 +164,7 @@ __global__ void __launch_bounds__(ALONE ? kAppendAlone * 32 : kAppendMaxWarps * 
   if (cached && !locate_row(p.c, seq, pos, &page, &off)) return;
   for (int i = ALONE ? lane : threadIdx.x; i < p.rot_chunks * 8; i += ALONE ? 32 : blockDim.x) {
     float c, s;
-    turn_cos_sin(pos, __ldg(p.turns + i), p.attn_factor, c, s);
+    turn_cos_sin(pos, p.turns[i], p.attn_factor, c, s);
     tab[0][(i & 7) * LH + (i >> 3)] = c;
     tab[1][(i & 7) * LH + (i >> 3)] = s;
   }
@@ -254,12 +255,13 @@ __global__ void __launch_bounds__(ALONE ? kAppendAlone * 32 : kAppendMaxWarps * 
 template <int D, bool Q4>
 __global__ void __launch_bounds__(kKvThreads) kv_gather_kernel(const GatherParams p) {
   constexpr int LH = D / 16, HW = 32 / LH;
+  start_behind_previous_kernel();
   const int gw = blockIdx.x * (kKvThreads / 32) + (threadIdx.x >> 5);
   const int t = gw / p.warps_per_token, part = gw - t * p.warps_per_token;
   if (t >= p.T) return;
   const int lane = threadIdx.x & 31, j = lane % LH, hs = lane / LH;
   int page, off;
-  if (!locate_row(p.c, __ldg(p.seq_ids + t), __ldg(p.positions + t), &page, &off)) return;
+  if (!locate_row(p.c, p.seq_ids[t], p.positions[t], &page, &off)) return;
   const size_t ob = (size_t)(t / p.out_len), oi = (size_t)(t % p.out_len);
   const int units = 2 * p.c.Hkv;
   for (int u = part * HW + hs; u < units; u += p.warps_per_token * HW) {

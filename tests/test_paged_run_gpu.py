@@ -227,3 +227,117 @@ def test_debug_build_matches_release(int4, tsf):
         outs.append([y.k_pages, y.v_pages, kr, vr] + [x[n] for x in got for n in ("o", "lse", "counts")])
     for a, b in zip(*outs):
         assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
+@pytest.mark.parametrize("int4", [False, True])
+@pytest.mark.parametrize("splits", [1, 4, 12])
+def test_calls_in_a_row_see_what_the_calls_before_wrote(int4, splits):
+    """Each call reads what the one before it wrote, with nothing in between
+    (their launches overlap); the same calls, waited for one by one, agree."""
+    steps, outs = 60, []
+    for wait in (True, False):
+        y = Layer(int4=int4, seed=21, B=2)
+        y.k_pages.zero_()
+        y.v_pages.zero_()
+        q, k, v = (x.contiguous() for x in y.qkv(y.B))
+        o = [q] + [torch.empty_like(q) for _ in range(steps)]
+        ks = [k] + [torch.empty_like(k) for _ in range(steps)]
+        vs = [v] + [torch.empty_like(v) for _ in range(steps)]
+        qr, lse = torch.empty_like(q), torch.empty(y.B, y.Hq, device="cuda")
+        seq = i32(range(y.B))
+        pos, lens = ([i32([n + i] * y.B) for n in range(steps)] for i in (0, 1))
+        ws = torch.empty(sk.sskip_attn_decode_workspace_size(y.B, y.Hq, y.d, splits), device="cuda",
+                         dtype=torch.uint8) if splits > 1 else None
+        done = torch.cuda.synchronize if wait else lambda: None
+        done()
+        for n in range(steps):
+            sk.sskip_kv_append(o[n], ks[n], vs[n], seq, pos[n], q_out=qr, k_pages=y.k_pages,
+                               v_pages=y.v_pages, block_table=y.table, **y.rope)
+            done()
+            sk.sskip_kv_gather(y.k_pages, y.v_pages, y.table, seq, pos[n], ks[n + 1], vs[n + 1])
+            done()
+            sk.sskip_attn_decode_paged(qr, y.k_pages, y.v_pages, y.table, lens[n], o[n + 1], lse,
+                                       sm_scale=y.scale, threshold_scale_factor=2.0,
+                                       num_splits=splits, workspace=ws)
+            done()
+        torch.cuda.synchronize()
+        outs.append([torch.stack(o), torch.stack(ks), torch.stack(vs), y.k_pages, y.v_pages])
+    assert sk.sskip_get_status() == sk.SSKIP_OK
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+    assert bool(torch.isfinite(outs[0][0].float()).all())
+
+
+@pytest.mark.parametrize("int4", [False, True])
+def test_captured_behind_copies_fills_and_joined_streams(int4):
+    """The calls as nodes of a graph whose other nodes are no kernels, or
+    come from another stream, replayed on new inputs."""
+    y = Layer(int4=int4, seed=23, B=3)
+    y.k_pages.zero_()
+    y.v_pages.zero_()
+    B, T = y.B, y.B * 40
+    src = [[x.contiguous() for x in y.qkv(T)] for _ in range(3)]
+    q, k, v = (torch.zeros_like(x) for x in src[0])
+    seq, pos = i32(np.repeat(np.arange(B), 40)), i32(np.tile(np.arange(40), B))
+    lens = i32([40] * B)
+    fresh = lambda: [torch.empty_like(q), torch.empty_like(k), torch.empty_like(v),  # noqa: E731
+                     torch.empty(B, y.Hq, y.d, device="cuda", dtype=torch.bfloat16),
+                     torch.empty(B, y.Hq, device="cuda")]
+    out, last = fresh(), torch.zeros(B, y.Hq, y.d, device="cuda", dtype=torch.bfloat16)
+
+    def append(st):
+        sk.sskip_kv_append(q, k, v, seq, pos, q_out=out[0], k_pages=y.k_pages, v_pages=y.v_pages,
+                           block_table=y.table, stream=st, **y.rope)
+
+    def gather(st):
+        sk.sskip_kv_gather(y.k_pages, y.v_pages, y.table, seq, pos, out[1], out[2], stream=st)
+
+    def decode(st):
+        sk.sskip_attn_decode_paged(last, y.k_pages, y.v_pages, y.table, lens, out[3], out[4],
+                                   sm_scale=y.scale, threshold_scale_factor=1.0, num_splits=1,
+                                   stream=st)
+
+    def run(new):
+        for x, n in zip((q, k, v), new):
+            x.copy_(n)
+        append(None)
+        last.copy_(out[0].view(B, 40, y.Hq, y.d)[:, -1])
+        gather(None)
+        decode(None)
+
+    inputs = [torch.empty_like(x) for x in src[0]]
+    side = torch.cuda.Stream()
+    run(src[0])
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        y.k_pages.zero_()                       # a fill
+        for x, n in zip((q, k, v), inputs):     # copies
+            x.copy_(n)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            y.v_pages.zero_()
+        main.wait_stream(side)                  # a join, the fill last
+        append(None)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):           # a fork: gather beside the decode
+            gather(side)
+        last.copy_(out[0].view(B, 40, y.Hq, y.d)[:, -1])
+        decode(None)
+        main.wait_stream(side)
+        out[4].add_(0.0)                        # a kernel behind the join
+        decode(None)                            # and a call behind a call
+    for new in src:
+        for x, n in zip(inputs, new):
+            x.copy_(n)
+        g.replay()
+        got = [x.clone() for x in out]
+        y.k_pages.zero_()
+        y.v_pages.zero_()
+        run(new)
+        for a, b in zip(got, out):
+            assert torch.equal(a, b)
+    torch.cuda.synchronize()
+    assert sk.sskip_get_status() == sk.SSKIP_OK
+    del g
