@@ -2,8 +2,8 @@
 // and packs them into the argument structs of include/sskip_attn.h.
 //
 // The calls of a decode step are a few microseconds long on the GPU; checking
-// and packing fourteen tensors from Python takes longer than that (8 us of an
-// 11.5 us append), from here about half a microsecond.  Nothing is computed or
+// and packing fourteen tensors from Python takes longer than that (an append of
+// 64 tokens 11.0 us a call, from here 4.7, of which the launch is 3.3).  Nothing is computed or
 // kept here.  The C functions come as addresses, so that the release and the
 // debug library share this file.
 #define PY_SSIZE_T_CLEAN

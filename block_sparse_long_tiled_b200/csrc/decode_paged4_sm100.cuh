@@ -10,7 +10,8 @@
 // two with one) cover the time a tile takes to arrive.  Measured at 64
 // sequences of 16K-32K (8 kv heads, d = 128, no threshold): half tiles in two
 // slots and 12 warps an SM 448 us, whole tiles in one slot 434, with 16 warps
-// 429.
+// 429; as it stands 396 us, 5.1 TB/s, at 320 instructions for 16 keys of a head
+// (55 % of the issue slots; 362 us with every tile in L2).
 //
 // Codes.  A bf16 whose sign and upper seven exponent bits are 0 is its low byte
 // times 2^-133: the subnormals and the first binade are evenly spaced.  So a
@@ -38,10 +39,15 @@
 // more product, of the record's (sc, mn) pairs with P in bf16 (for d = 64, where
 // a key's pairs do not fill a row of an 8x8 matrix, a sum in fp32).
 //
-// With a threshold the warps take one decision for four tiles at a time: each
-// publishes its tile's maxima, and after one named barrier all walk the four
-// tiles in order under the rule.  The scores wait in shared memory for the V
-// tile, which is fetched after the decision and used one round later.
+// With a threshold the warps go in rounds of four tiles.  Each works out its
+// tile's scores, which wait in shared memory; then a record of every kept tile
+// of the ROUND BEFORE, so that a tile few warps would keep busy is shared by
+// all; then it publishes its tile's maxima, and after the round's one barrier
+// all walk the four tiles in order under the rule (a head a lane).  The barrier
+// also says that the V slots are read, and a kept tile's V is fetched behind it.
+// Factor 500 (63 % skipped), same workload: 368 us; 395 with a kept tile's V
+// worked on by its own warp, 391 with the barrier ahead of the V work and a
+// second one, 490 with 15 or 16 warps of 136 or 128 registers an SM.
 #pragma once
 
 #include <type_traits>

@@ -837,7 +837,7 @@ bool make_page_map(CUtensorMap* map, const void* base, int d, long long rows, in
 // Launch a kernel that begins with start_behind_previous_kernel(): it is brought
 // up while the kernel before it in the stream runs, and waits for that one's end
 // on the device.  Calls in a row come a trip of the launch closer together (a
-// short decode 8.2 -> 6.1 us a call).  cluster: CTAs along x, 1 for none.
+// short decode 8.2 -> 6.2 us a call).  cluster: CTAs along x, 1 for none.
 template <typename... Params, typename... Args>
 int launch_behind(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t st,
                   int cluster, Args&&... args) {
