@@ -721,12 +721,13 @@ def prefill_paged(q, k, v, seq_ids, positions, k_pages, v_pages, block_table, *,
                   Br: int = 128, Bc: int = 128, stream=None) -> dict:
     """A batch of whole prompts of L tokens each, from projections q [B L,Hq,d],
     k, v [B L,Hkv,d]: append to the paged cache (norm, rotation) and causal
-    prefill of what was appended. Returns prefill's outputs."""
+    prefill of what was appended. A shorter prompt ends in padding (seq_ids < 0),
+    whose output rows mean nothing. Returns prefill's outputs."""
     T, Hq, d = q.shape
     Hkv = k.shape[1]
-    with _alloc_on(stream):
-        qr = torch.empty((T // L, Hq, L, d), dtype=q.dtype, device=q.device)
-        kr, vr = (torch.empty((T // L, Hkv, L, d), dtype=q.dtype, device=q.device)
+    with _alloc_on(stream):  # rows of padding stay 0: their tile's other rows meet them
+        qr = torch.zeros((T // L, Hq, L, d), dtype=q.dtype, device=q.device)
+        kr, vr = (torch.zeros((T // L, Hkv, L, d), dtype=q.dtype, device=q.device)
                   for _ in range(2))
     sskip_kv_append(q, k, v, seq_ids, positions, q_out=qr, k_out=kr, v_out=vr, k_pages=k_pages,
                     v_pages=v_pages, block_table=block_table, turns=turns, interleaved=interleaved,
@@ -743,8 +744,8 @@ def decode_step_paged(q, k, v, seq_ids, positions, seqlens, k_pages, v_pages, bl
                       stream=None) -> dict:
     """One decode step of a layer: append the new token of every sequence
     (q [B,Hq,d], k, v [B,Hkv,d], positions[b] = seqlens[b] - 1) and attend over
-    the cache, the new token included. A padded batch entry has seq_ids[b] < 0
-    and seqlens[b] = 0. Returns decode_paged's outputs."""
+    the cache, the new token included. Entry b is sequence b: seq_ids[b] = b, or
+    for a padded entry seq_ids[b] < 0 and seqlens[b] = 0. Returns decode_paged's outputs."""
     with _alloc_on(stream):
         qr = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
     sskip_kv_append(q, k, v, seq_ids, positions, q_out=qr, k_pages=k_pages, v_pages=v_pages,

@@ -341,3 +341,30 @@ def test_captured_behind_copies_fills_and_joined_streams(int4):
     torch.cuda.synchronize()
     assert sk.sskip_get_status() == sk.SSKIP_OK
     del g
+
+
+@pytest.mark.parametrize("tsf", [0.0, 2.0])
+def test_shorter_prompts_end_in_padding(tsf):
+    """What stood in the memory before does not reach the rows of a prompt
+    whose last rows are padding."""
+    y = Layer(seed=25, B=2)
+    L, n = 200, 131
+    q, k, v = y.qkv(2 * L)
+    seq, pos = np.repeat([0, 1], L), np.tile(np.arange(L), 2)
+    seq[L + n:] = -1
+    outs = []
+    for fill in (float("nan"), 0.0):
+        dirt = [torch.full((2, h, L, y.d), fill, device="cuda", dtype=torch.bfloat16)
+                for h in (y.Hq, y.Hkv, y.Hkv, y.Hq)]
+        del dirt
+        out = sk.prefill_paged(q, k, v, i32(seq), i32(pos), y.k_pages, y.v_pages, y.table, L=L,
+                               sm_scale=y.scale, threshold_scale_factor=tsf, **y.rope)
+        outs.append([out["o"][0], out["o"][1, :, :n], out["lse"][0], out["lse"][1, :, :n]])
+    assert sk.sskip_get_status() == sk.SSKIP_OK
+    for a, b in zip(*outs):
+        assert bool(torch.isfinite(a.float()).all()) and torch.equal(a, b)
+    if tsf == 0.0:  # and they are what real tokens behind them would leave them
+        seq[L + n:] = 1
+        full = sk.prefill_paged(q, k, v, i32(seq), i32(pos), y.k_pages, y.v_pages, y.table, L=L,
+                                sm_scale=y.scale, threshold_scale_factor=tsf, **y.rope)
+        assert torch.equal(outs[0][1], full["o"][1, :, :n])
