@@ -1117,6 +1117,19 @@ SSKIP_API int sskip_attn_decode_paged(const sskip_decode_paged_args* args, void*
   if (num_splits > 1 &&
       (!workspace || workspace_bytes < sskip_attn_decode_workspace_size(B, Hq, d, num_splits)))
     return SSKIP_ERR_INVALID_ARG;
+  // The CTAs of a call write while others still read.
+  const size_t heads = (size_t)B * Hq;
+  const size_t pages = num_pages * sskip_kv_page_bytes(kv_format, Hkv, page_size, d);
+  const bool split = num_splits > 1;
+  const struct { const void* p; size_t n; } range[] = {
+      {o, heads * d * 2},
+      {lse, heads * 4},
+      {split ? workspace : nullptr,
+       split ? sskip_attn_decode_workspace_size(B, Hq, d, num_splits) : 0},
+      {q, heads * d * 2}, {k_pages, pages}, {v_pages, pages}};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 6; ++j)
+      if (overlap(range[i].p, range[i].n, range[j].p, range[j].n)) return SSKIP_ERR_INVALID_ARG;
 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const size_t rows = (size_t)B * Hq * num_splits;

@@ -529,6 +529,8 @@ int sskip_kv_gather(const sskip_kv_gather_args* args, void* stream);
  * in either format.
  *
  *   q [B, Hq, d], o [B, Hq, d] bf16, lse [B, Hq] fp32 natural log.
+ *     No two of o, lse and the workspace, nor one of them and q or the pages,
+ *     may overlap.
  *   seqlens [B] int32 on the device, 0 <= seqlens[b] <= max_pages * page_size.
  *     0 gives O = 0 and lse = -inf (a padded batch entry).  Another length is
  *     latched and clamped; a page outside the pool is latched and read as page

@@ -144,6 +144,9 @@ def decode(lib, **kw):
     (dict(scale=0.0), INVALID), (dict(tsf=-1.0), INVALID), (dict(tsf=float("nan")), INVALID),
     (dict(B=0), INVALID), (dict(d=80), UNSUPPORTED), (dict(P=80), UNSUPPORTED),
     (dict(fmt=7), UNSUPPORTED), (dict(B=70000), UNSUPPORTED), (dict(fmt=1, scale=1e13), UNSUPPORTED),
+    (dict(o=at(0)), INVALID), (dict(o=at(0, 16)), INVALID), (dict(lse=at(0, 4)), INVALID),
+    (dict(o=at(2, 1024)), INVALID), (dict(ws=at(1)), INVALID), (dict(ws=at(5)), INVALID),
+    (dict(lse=at(5, 2 * 8 * 128 * 2 - 4)), INVALID),
 ], ids=str)
 def test_decode_refuses(lib, kw, rc):
     assert decode(lib, **kw) == rc
