@@ -133,6 +133,18 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
   const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+  const uint32_t bars = smem_u32(smem + C::kBar) + warp * 2 * 8;  // this warp's
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kBar + W * 2 * 8);
+  // Shared-memory addresses (32 bits: the loads' arithmetic stays short).
+  const uint32_t kbuf = smem_u32(smem + C::kK) + warp * C::kBytes;
+  const uint32_t vbuf = smem_u32(smem + C::kV) + warp * C::kBytes;
+  if (lane == 0) {
+    mbar_init(bars, 1);
+    mbar_init(bars + 8, 1);
+    if (warp == 0) *abort_flag = 0;
+    fence_mbar_init();
+  }
+
   start_behind_previous_kernel();
   // seqlens[b] lies in [0, max_pages * P]: another length is latched and
   // clamped, so that no page number is read outside the sequence's table row.
@@ -154,18 +166,6 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
   }
   const int key0 = j0 * kPgTile;                              // of the split
   const int keys = min(Lb, (j0 + ntiles) * kPgTile) - key0;
-
-  const uint32_t bars = smem_u32(smem + C::kBar) + warp * 2 * 8;  // this warp's
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kBar + W * 2 * 8);
-  // Shared-memory addresses (32 bits: the loads' arithmetic stays short).
-  const uint32_t kbuf = smem_u32(smem + C::kK) + warp * C::kBytes;
-  const uint32_t vbuf = smem_u32(smem + C::kV) + warp * C::kBytes;
-  if (lane == 0) {
-    mbar_init(bars, 1);
-    mbar_init(bars + 8, 1);
-    if (warp == 0) *abort_flag = 0;
-    fence_mbar_init();
-  }
   __syncthreads();
 
   // ---- the copies of a tile: one when a page holds it, else 64 / P, of which

@@ -264,6 +264,27 @@ __global__ void __launch_bounds__(kPgThreads, PagedCfg<D>::kCtas)
   const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBar);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kBar + 4 * NS * 8);
+  int* ids = reinterpret_cast<int*>(smem + C::kIds);
+  const uint32_t k_smem = smem_u32(smem + C::kK), v_smem = smem_u32(smem + C::kV);
+  auto kfull = [&](int s) { return smem_u32(&bars[s]); };
+  auto kfree = [&](int s) { return smem_u32(&bars[NS + s]); };
+  auto vfull = [&](int s) { return smem_u32(&bars[2 * NS + s]); };
+  auto vfree = [&](int s) { return smem_u32(&bars[3 * NS + s]); };
+  if (tid == 0) {
+    tma_prefetch_desc(&map_k);
+    tma_prefetch_desc(&map_v);
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(kfull(s), 1);
+      mbar_init(kfree(s), kPgWarps);
+      mbar_init(vfull(s), 1);
+      mbar_init(vfree(s), kPgWarps);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+
   start_behind_previous_kernel();
   // seqlens[b] lies in [0, max_pages * P]: another length is latched and
   // clamped, so that no page number is read outside the sequence's table row.
@@ -283,25 +304,6 @@ __global__ void __launch_bounds__(kPgThreads, PagedCfg<D>::kCtas)
     paged_empty_split<D>(p, part, head0, split, tid, kPgThreads);
     if (p.clustered) paged_cluster_merge<D>(p, part, head0, tid, kPgThreads);
     return;
-  }
-
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBar);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kBar + 4 * NS * 8);
-  int* ids = reinterpret_cast<int*>(smem + C::kIds);
-  const uint32_t k_smem = smem_u32(smem + C::kK), v_smem = smem_u32(smem + C::kV);
-  auto kfull = [&](int s) { return smem_u32(&bars[s]); };
-  auto kfree = [&](int s) { return smem_u32(&bars[NS + s]); };
-  auto vfull = [&](int s) { return smem_u32(&bars[2 * NS + s]); };
-  auto vfree = [&](int s) { return smem_u32(&bars[3 * NS + s]); };
-  if (tid == 0) {
-    for (int s = 0; s < NS; ++s) {
-      mbar_init(kfull(s), 1);
-      mbar_init(kfree(s), kPgWarps);
-      mbar_init(vfull(s), 1);
-      mbar_init(vfree(s), kPgWarps);
-    }
-    *abort_flag = 0;
-    fence_mbar_init();
   }
   __syncthreads();
 

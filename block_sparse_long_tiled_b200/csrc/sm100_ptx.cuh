@@ -140,12 +140,13 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-// The first statement of a kernel that is launched dependently: its launch
-// overlaps the kernel before it in the stream, whose end and writes it waits for
-// here; the next kernel, if launched so too, may start once every CTA has come
-// this far.  All threads call it, before any return, so that a kernel's end
-// implies the end of all before it.  Such a kernel reads nothing through the
-// read-only path (__ldg): that may be moved ahead of the wait.
+// Called by a kernel that is launched dependently, before it reads or writes
+// global memory: its launch and what stands ahead of this (barriers, tensor map
+// prefetches) overlap the kernel before it in the stream, whose end and writes
+// it waits for here; the next kernel, if launched so too, may start once every
+// CTA has come this far.  All threads call it, before any return, so that a
+// kernel's end implies the end of all before it.  Such a kernel reads nothing
+// through the read-only path (__ldg): that may be moved ahead of the wait.
 __device__ __forceinline__ void start_behind_previous_kernel() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
