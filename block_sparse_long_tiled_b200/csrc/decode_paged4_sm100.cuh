@@ -62,7 +62,10 @@ constexpr int kP4Threads = kP4Warps * 32;
 template <int D, bool SKIP>
 struct Paged4Cfg {
   static constexpr int kBytes = 4 * Kv4<D>::kRecord;          // of a tile
-  static constexpr int kCtas = SKIP ? 3 : 4;                  // per SM
+  // Per SM: as many as registers and shared memory hold without slowing the
+  // code (d = 64, 64 x 16K-32K: 247 us with five, 262 with four, 253 with six;
+  // at factor 500 263 with four, 297 with three, 267 with five).
+  static constexpr int kCtas = (SKIP ? 3 : 4) + (D == 64 ? 1 : 0);
   static constexpr int kK = 0;                                // [W] tiles
   static constexpr int kV = kK + kP4Warps * kBytes;
   static constexpr int kS = kV + kP4Warps * kBytes;           // [2][W][64][8] fp32 scores
