@@ -50,13 +50,20 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
+__device__ __forceinline__ float min_nan(float a, float b, float c) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 __device__ __forceinline__ void kv4_bounds(const float (&x)[8], float& lo, float& hi) {
-  lo = hi = x[0];
-#pragma unroll
-  for (int e = 1; e < 8; ++e) {
-    lo = min_nan(lo, x[e]);
-    hi = max_nan(hi, x[e]);
-  }
+  lo = min_nan(min_nan(x[0], x[1], x[2]), min_nan(x[3], x[4], x[5]), min_nan(x[6], x[7]));
+  hi = max_nan(max_nan(x[0], x[1], x[2]), max_nan(x[3], x[4], x[5]), max_nan(x[6], x[7]));
 }
 
 // rint(y / sc), ties to even, for 0 <= y <= about 15 sc, in the low bits of a
@@ -66,12 +73,14 @@ __device__ __forceinline__ void kv4_bounds(const float (&x)[8], float& lo, float
 // System/6000 processor", 1990; scales within 2^23 of the smallest can have a
 // subnormal, so inexact, remainder, and then an ulp is off).  One division a
 // group, not one a value: the reciprocal unit takes 8 clocks of a sub-partition
-// for a warp.
+// for a warp.  No clamp: sc is (max - mn) / 15 to an ulp at least, so no quotient
+// of a finite group comes near 15.5; one that holds a NaN or an infinity leaves
+// any codes, in words of its own, under a scale that is NaN.
 constexpr uint32_t kCodeBias = 0x4B400000u;  // 1.5 * 2^23: adding it rounds to an integer
 __device__ __forceinline__ uint32_t kv4_code(float y, float sc, float inv) {
   const float q = y * inv;
   const float exact = fmaf(fmaf(-q, sc, y), inv, q);
-  return __float_as_uint(fminf(exact, 15.f) + __uint_as_float(kCodeBias));
+  return __float_as_uint(exact + __uint_as_float(kCodeBias));
 }
 
 // Store row r of a record.  The D / 16 lanes of a head hold chunks m0 and m1
