@@ -148,7 +148,8 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
     fence_mbar_init();
   }
 
-  start_behind_previous_kernel();
+  wait_for_previous_kernel();
+  launch_dependents();
   // seqlens[b] lies in [0, max_pages * P]: another length is latched and
   // clamped, so that no page number is read outside the sequence's table row.
   const int cap = p.c.max_pages << p.c.page_shift;

@@ -285,7 +285,8 @@ __global__ void __launch_bounds__(kPgThreads, PagedCfg<D>::kCtas)
     fence_mbar_init();
   }
 
-  start_behind_previous_kernel();
+  wait_for_previous_kernel();
+  launch_dependents();
   // seqlens[b] lies in [0, max_pages * P]: another length is latched and
   // clamped, so that no page number is read outside the sequence's table row.
   const int cap = p.c.max_pages << p.c.page_shift;
@@ -607,7 +608,8 @@ __global__ void __launch_bounds__(128) decode_paged_combine_kernel(const PagedDe
   __shared__ float w_s[64];
   __shared__ float red[4][D];
   __shared__ float sum_s;
-  start_behind_previous_kernel();
+  wait_for_previous_kernel();
+  launch_dependents();
   if (warp == 0) {
     const float a = lane < p.S ? lp[lane] : -INFINITY;
     const float e = lane + 32 < p.S ? lp[lane + 32] : -INFINITY;

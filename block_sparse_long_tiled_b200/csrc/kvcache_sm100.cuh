@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(ALONE ? kAppendAlone * 32 : kAppendMaxWarps * 
     kv_append_kernel(const AppendParams p) {
   constexpr int LH = D / 16;       // lanes per head
   constexpr int HW = 32 / LH;      // heads a warp holds at a time
-  start_behind_previous_kernel();
+  wait_for_previous_kernel();
   // cosine and sine of pair 8 j + e at e LH + j
   __shared__ float tabs[ALONE ? kAppendAlone : 1][2][D / 2];
   const int lane = threadIdx.x & 31, j = lane % LH, hs = lane / LH;
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(ALONE ? kAppendAlone * 32 : kAppendMaxWarps * 
 template <int D, bool Q4>
 __global__ void __launch_bounds__(kKvThreads) kv_gather_kernel(const GatherParams p) {
   constexpr int LH = D / 16, HW = 32 / LH;
-  start_behind_previous_kernel();
+  wait_for_previous_kernel();
   const int gw = blockIdx.x * (kKvThreads / 32) + (threadIdx.x >> 5);
   const int t = gw / p.warps_per_token, part = gw - t * p.warps_per_token;
   if (t >= p.T) return;

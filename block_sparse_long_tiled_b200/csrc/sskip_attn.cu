@@ -834,7 +834,7 @@ bool make_page_map(CUtensorMap* map, const void* base, int d, long long rows, in
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Launch a kernel that begins with start_behind_previous_kernel(): it is brought
+// Launch a kernel that begins with wait_for_previous_kernel(): it is brought
 // up while the kernel before it in the stream runs, and waits for that one's end
 // on the device.  Calls in a row come a trip of the launch closer together (a
 // short decode 8.2 -> 6.2 us a call).  cluster: CTAs along x, 1 for none.
