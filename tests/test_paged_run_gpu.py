@@ -368,3 +368,34 @@ def test_shorter_prompts_end_in_padding(tsf):
         full = sk.prefill_paged(q, k, v, i32(seq), i32(pos), y.k_pages, y.v_pages, y.table, L=L,
                                 sm_scale=y.scale, threshold_scale_factor=tsf, **y.rope)
         assert torch.equal(outs[0][1], full["o"][1, :, :n])
+
+
+@pytest.mark.parametrize("tsf", [0.0, 2.0])
+@pytest.mark.parametrize("int4,pages", [(False, 40_000), (True, 110_000)])
+def test_pools_of_more_than_4_gib(int4, pages, tsf):
+    """Pages on both sides of byte 2^32 of a pool give what a small pool with
+    the same rows does."""
+    y = Layer(Hq=16, Hkv=8, P=64, B=3, int4=int4, seed=27)
+    M = y.table.shape[1]
+    assert pages * sk.sskip_kv_page_bytes(sk.SSKIP_KV_INT4 if int4 else sk.SSKIP_KV_BF16, 8, 64,
+                                          128) > 2 ** 32
+    far = sk.paged_cache(pages, 8, 64, 128, int4=int4)
+    far_table = torch.linspace(0, pages - 1, 3 * M).int().reshape(M, 3).t().contiguous().cuda()
+    lens = [290, 64, 201]
+    seq = np.concatenate([np.full(n, b) for b, n in enumerate(lens)])
+    pos = np.concatenate([np.arange(n) for n in lens])
+    q, k, v = y.qkv(len(seq))
+    q1 = y.qkv(3)[0].contiguous()
+    got = []
+    for (kp, vp), table in (((y.k_pages, y.v_pages), y.table), (far, far_table)):
+        sk.sskip_kv_append(None, k, v, i32(seq), i32(pos), k_pages=kp, v_pages=vp, block_table=table,
+                           turns=y.rope["turns"], k_weight=y.rope["k_weight"])
+        rows = [torch.empty(len(seq), 8, 128, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+        sk.sskip_kv_gather(kp, vp, table, i32(seq), i32(pos), *rows)
+        out = sk.decode_paged(q1, kp, vp, table, i32(lens), sm_scale=y.scale,
+                              threshold_scale_factor=tsf, num_splits=3)
+        got.append(rows + [out["o"], out["lse"], out["counts"]])
+    torch.cuda.synchronize()
+    assert sk.sskip_get_status() == sk.SSKIP_OK
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
