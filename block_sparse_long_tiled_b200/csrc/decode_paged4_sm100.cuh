@@ -7,7 +7,10 @@
 // producer, every warp owns WHOLE tiles and fetches them itself into a slot
 // that only it uses, so that waits, reference checks and votes spread over 64
 // keys, and the other warps of its sub-partition (three without a threshold,
-// two with one) cover the time a tile takes to arrive.  Measured at 64
+// two with one) cover the time a tile takes to arrive.  A call of two CTAs an SM
+// at most, without a threshold, has too few warps for that: there (DEEP) a warp
+// has two slots, one arriving while it works on the other (128K keys, 8 kv heads,
+// 18 splits 76 -> 59 us, 37 splits 53 -> 47).  Measured at 64
 // sequences of 16K-32K (8 kv heads, d = 128, no threshold): half tiles in two
 // slots and 12 warps an SM 448 us, whole tiles in one slot 434, with 16 warps
 // 429; as it stands 396 us, 5.1 TB/s, at 320 instructions for 16 keys of a head
@@ -59,16 +62,17 @@ namespace sskip {
 constexpr int kP4Warps = 4;
 constexpr int kP4Threads = kP4Warps * 32;
 
-template <int D, bool SKIP>
+template <int D, bool SKIP, bool DEEP>
 struct Paged4Cfg {
   static constexpr int kBytes = 4 * Kv4<D>::kRecord;          // of a tile
   // Per SM: as many as registers and shared memory hold without slowing the
   // code (d = 64, 64 x 16K-32K: 247 us with five, 262 with four, 253 with six;
   // at factor 500 263 with four, 297 with three, 267 with five).
-  static constexpr int kCtas = (SKIP ? 3 : 4) + (D == 64 ? 1 : 0);
-  static constexpr int kK = 0;                                // [W] tiles
-  static constexpr int kV = kK + kP4Warps * kBytes;
-  static constexpr int kS = kV + kP4Warps * kBytes;           // [2][W][64][8] fp32 scores
+  static constexpr int kCtas = DEEP ? 2 : (SKIP ? 3 : 4) + (D == 64 ? 1 : 0);
+  static constexpr int kSlots = DEEP ? 2 : 1;                 // tiles of a warp
+  static constexpr int kK = 0;                                // [W][kSlots] tiles
+  static constexpr int kV = kK + kP4Warps * kSlots * kBytes;
+  static constexpr int kS = kV + kP4Warps * kSlots * kBytes;           // [2][W][64][8] fp32 scores
   static constexpr int kMax = kS + (SKIP ? kP4Warps * 2 * kPgTile * 8 * 4 : 0);  // [2][8][W]
   // The two merges reuse the slots and the scores.
   static constexpr int kPart = kP4Warps * 8 * (D + 4) * 4;
@@ -123,10 +127,11 @@ __device__ __forceinline__ void lds_words(uint32_t (&w)[N], uint32_t addr) {
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
 }
 
-template <int D, bool SKIP>
-__global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
+template <int D, bool SKIP, bool DEEP>
+__global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP, DEEP>::kCtas)
     decode_paged4_kernel(const PagedDecodeParams p) {
-  using C = Paged4Cfg<D, SKIP>;
+  using C = Paged4Cfg<D, SKIP, DEEP>;
+  static_assert(!(SKIP && DEEP), "a threshold has one tile of keys in flight");
   constexpr int W = kP4Warps, UNIT = kPgTile, NREC = UNIT / 16;
   constexpr int NG = D / 32;   // groups of a row
   constexpr int MT = D / 16;   // 16-row tiles of O^T
@@ -139,8 +144,8 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
   const uint32_t bars = smem_u32(smem + C::kBar) + warp * 2 * 8;  // this warp's
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kBar + W * 2 * 8);
   // Shared-memory addresses (32 bits: the loads' arithmetic stays short).
-  const uint32_t kbuf = smem_u32(smem + C::kK) + warp * C::kBytes;
-  const uint32_t vbuf = smem_u32(smem + C::kV) + warp * C::kBytes;
+  const uint32_t kbuf = smem_u32(smem + C::kK) + warp * C::kSlots * C::kBytes;
+  const uint32_t vbuf = smem_u32(smem + C::kV) + warp * C::kSlots * C::kBytes;
   if (lane == 0) {
     mbar_init(bars, 1);
     mbar_init(bars + 8, 1);
@@ -187,11 +192,13 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
   const uint32_t dst = ((lane & 4) ? vbuf : kbuf) + sub * copy_bytes;
   // key: this lane's first key of a tile.  Nothing looks at the number before
   // the copy is issued: the look-up is a trip to memory.
+  // key: this lane's first key of a tile.  The number is looked at when its copy
+  // is issued, not here: the look-up is a trip to memory.
   auto page_at = [&](int key) { return copies && key < end ? table[key >> shift] : 0; };
   // The tile whose first key (of lane sub = 0) is k0, this lane's being `key`.
-  // which: bit 0 K, bit 1 V.  Called by the whole warp, on a slot whose last
-  // copies have arrived.
-  auto fetch = [&](int k0, int key, int page, int which, uint32_t bar) {
+  // which: bit 0 K, bit 1 V; slot: of the warp's.  Called by the whole warp, on a
+  // slot whose last copies have arrived.
+  auto fetch = [&](int k0, int key, int page, int which, uint32_t bar, int slot) {
     const bool ok = dev_check(k0 < end);
     if (lane == 0) {
       const uint32_t n = (uint32_t)min(UNIT, (end - k0 + rows - 1) >> row_shift << row_shift);
@@ -204,7 +211,7 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
         latch_status(kStatusInvalidArg);  // read as page 0
         page = 0;
       }
-      bulk_load(dst,
+      bulk_load(dst + slot * C::kBytes,
                 pool + (size_t)page * page_bytes +
                     (uint32_t)(key & ((1 << shift) - 1)) * (uint32_t)(REC / 16),
                 copy_bytes, bar);
@@ -220,20 +227,25 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
   constexpr int STEP = W * UNIT;
   int key = key0 + u * UNIT + sub * rows;  // this lane's first key of the next tile to fetch
   int page = page_at(key), next_page = 0;  // of that tile and the one after it
-  bool k_inflight = false;                 // K's tile, or the tile
-  if (u < ntiles) {
-    fetch(key0 + u * UNIT, key, page, SKIP ? 1 : 3, bars);
-    k_inflight = true;
-    next_page = page_at(key + STEP);
-  }
-  // The next tile into the slot just read.
-  auto fetch_next = [&] {
-    key += STEP;
-    page = next_page;
-    fetch(key0 + (u + W) * UNIT, key, page, SKIP ? 1 : 3, bars);
+  bool k_inflight = false;                 // SKIP: K's tile
+  // This warp's next tile, `tile` of the split, into a slot that has been read;
+  // then the look-up for the one after it.
+  auto fetch_next = [&](int tile, int slot) {
+    fetch(key0 + tile * UNIT, key, page, SKIP ? 1 : 3, bars + slot * 8, slot);
     k_inflight = true;
     next_page = page_at(key + STEP);
   };
+  auto step = [&] {
+    key += STEP;
+    page = next_page;
+  };
+  if (u < ntiles) {
+    fetch_next(u, 0);
+    if (DEEP && u + W < ntiles) {
+      step();
+      fetch_next(u + W, 1);
+    }
+  }
 
   // ---- Q^T of head g: the d's that the key words hold at this lane, times 2^48
   // (even nibbles) or 2^44 (odd ones): a power of two, so still exact.
@@ -429,26 +441,34 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
       l[1] += pr[1] + pr[3];
       accumulate(tail, vrec, valid, pr);
     };
-    uint32_t parity = 0;
-    for (; u < ntiles; u += W, parity ^= 1) {
-      if (!await(bars, parity)) break;
-      k_inflight = false;
+    auto slot_of = [](int i) { return DEEP ? i & 1 : 0; };          // of the warp's tile i
+    auto phase_of = [](int i) { return (uint32_t)((DEEP ? i >> 1 : i) & 1); };
+    int n = 0;  // tiles done
+    for (; u < ntiles; u += W, ++n) {
+      const int slot = slot_of(n);
+      if (!await(bars + slot * 8, phase_of(n))) break;
+      const uint32_t kt = kbuf + slot * C::kBytes, vt = vbuf + slot * C::kBytes;
       const int left = keys - u * UNIT;
       if (left >= UNIT) {
 #pragma unroll 1
-        for (int i = 0; i < NREC; ++i) record(full, kbuf + i * REC, vbuf + i * REC, 16);
+        for (int i = 0; i < NREC; ++i) record(full, kt + i * REC, vt + i * REC, 16);
       } else {
 #pragma unroll 1
-        for (int i = 0; i * 16 < left; ++i) record(last, kbuf + i * REC, vbuf + i * REC, left - i * 16);
+        for (int i = 0; i * 16 < left; ++i) record(last, kt + i * REC, vt + i * REC, left - i * 16);
       }
       if (p.tile_state && lane == 0)
         p.tile_state[((size_t)b * p.Hkv + kvh) * p.n_k_max + j0 + u] = 1;
       __syncwarp();  // every lane is past its reads of the slot
-      if (u + W < ntiles) fetch_next();
+      if (u + C::kSlots * W < ntiles) {
+        step();
+        fetch_next(u + C::kSlots * W, slot);
+      }
     }
-    if (k_inflight) {  // gave up: wait out this warp's copies before the CTA exits
+    // Gave up: wait out this warp's copies, of tile u and (two slots) the one
+    // after it, before the CTA exits.
+    for (int i = 0; i < C::kSlots && u < ntiles; ++i, ++n, u += W) {
       int no_abort = 0;
-      mbar_wait(bars, parity, &no_abort);
+      mbar_wait(bars + slot_of(n) * 8, phase_of(n), &no_abort);
     }
   } else {
     float* wmax = reinterpret_cast<float*>(smem + C::kMax);
@@ -490,7 +510,10 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
         __syncwarp();  // every lane is past its reads of the slot
         vpage = page;
         vkey = key;
-        if (u + W < ntiles && there) fetch_next();
+        if (u + W < ntiles && there) {
+          step();
+          fetch_next(u + W, 0);
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -559,7 +582,7 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP>::kCtas)
         if (p.tile_state && lane == 0)
           p.tile_state[((size_t)b * p.Hkv + kvh) * p.n_k_max + j0 + u] = keep ? 1 : 2;
         if (keep && !v_inflight) {
-          fetch(key0 + u * UNIT, vkey, vpage, 2, bars + 8);
+          fetch(key0 + u * UNIT, vkey, vpage, 2, bars + 8, 0);
           v_inflight = true;
         }
       }

@@ -884,8 +884,13 @@ int launch_decode_paged(const CUtensorMap& mk, const CUtensorMap& mv, const Page
 
 template <int D, bool SKIP>
 int launch_decode_paged4(const PagedDecodeParams& p, cudaStream_t st) {
-  return launch_splits<D>(decode_paged4_kernel<D, SKIP>, kP4Threads, Paged4Cfg<D, SKIP>::kTotal, p,
-                          st, p);
+  if constexpr (!SKIP) {  // two CTAs an SM: a second slot for every warp
+    if ((long long)p.B * p.Hkv * p.S <= 2 * 148)
+      return launch_splits<D>(decode_paged4_kernel<D, false, true>, kP4Threads,
+                              Paged4Cfg<D, false, true>::kTotal, p, st, p);
+  }
+  return launch_splits<D>(decode_paged4_kernel<D, SKIP, false>, kP4Threads,
+                          Paged4Cfg<D, SKIP, false>::kTotal, p, st, p);
 }
 
 }  // namespace

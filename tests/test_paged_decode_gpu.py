@@ -140,6 +140,16 @@ def test_every_kind_of_last_tile(n, P, fmt):
 
 
 @FMT
+@pytest.mark.parametrize("kw", [dict(), dict(d=64, P=16), dict(splits=1, Hq=16, Hkv=16)], ids=str)
+def test_more_ctas_than_two_an_sm(kw, fmt):
+    # 320 or more: no clusters, and (4-bit) one slot a warp
+    kw = dict(dict(splits=10, Hq=16, Hkv=8), **kw)
+    lens = [2100, 0, 1, 65, 700, 64, 1025, 17] if kw["splits"] > 1 else [1025, 0, 1, 65] * 5
+    got = Case(lens[:4] if kw["splits"] > 1 else lens, fmt=fmt, **kw).check()
+    assert got["count"][0] == 0
+
+
+@FMT
 @pytest.mark.parametrize("tsf", [0.0, 500.0])
 def test_long_sequences(tsf, fmt):
     # rings go round many times, splits of uneven length
