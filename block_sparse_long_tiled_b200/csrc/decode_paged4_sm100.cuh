@@ -13,7 +13,7 @@
 // 18 splits 76 -> 59 us, 37 splits 53 -> 47).  Measured at 64
 // sequences of 16K-32K (8 kv heads, d = 128, no threshold): half tiles in two
 // slots and 12 warps an SM 448 us, whole tiles in one slot 434, with 16 warps
-// 429; as it stands 396 us, 5.1 TB/s, at 320 instructions for 16 keys of a head
+// 429; as it stands 397 us, 5.1 TB/s, at 320 instructions for 16 keys of a head
 // (55 % of the issue slots; 362 us with every tile in L2).
 //
 // Codes.  A bf16 whose sign and upper seven exponent bits are 0 is its low byte
@@ -228,12 +228,15 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP, DEEP>::kCtas)
   int key = key0 + u * UNIT + sub * rows;  // this lane's first key of the next tile to fetch
   int page = page_at(key), next_page = 0;  // of that tile and the one after it
   bool k_inflight = false;                 // SKIP: K's tile
-  // This warp's next tile, `tile` of the split, into a slot that has been read;
-  // then the look-up for the one after it.
+  // This warp's next tile, `tile` of the split, into a slot that has been read,
+  // and the look-up for the one after it (ahead of the copies where another tile
+  // is there to work on: 4 splits of 128K keys 178 us and 167; else behind them:
+  // 64 x 16K-32K 400 us and 397).
   auto fetch_next = [&](int tile, int slot) {
+    if (DEEP) next_page = page_at(key + STEP);
     fetch(key0 + tile * UNIT, key, page, SKIP ? 1 : 3, bars + slot * 8, slot);
     k_inflight = true;
-    next_page = page_at(key + STEP);
+    if (!DEEP) next_page = page_at(key + STEP);
   };
   auto step = [&] {
     key += STEP;
