@@ -500,8 +500,8 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP, DEEP>::kCtas)
           scores(tail, kbuf + i * REC, left - i * 16, x);
           *reinterpret_cast<float2*>(sb + i * 128) = make_float2(x[0], x[1]);
           *reinterpret_cast<float2*>(sb + i * 128 + 64) = make_float2(x[2], x[3]);
-          top[0] = fmaxf(top[0], fmaxf(x[0], x[2]));
-          top[1] = fmaxf(top[1], fmaxf(x[1], x[3]));
+          top[0] = max_nan(top[0], x[0], x[2]);
+          top[1] = max_nan(top[1], x[1], x[3]);
         };
         if (left >= UNIT) {
 #pragma unroll 2  // 371 us, 379 one by one, 376 by four
@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP, DEEP>::kCtas)
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1)
-            top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], o));
+            top[h] = max_nan(top[h], __shfl_xor_sync(0xffffffffu, top[h], o));
       }
       // The kept tiles of round r - 1, whose V tiles have had these scores'
       // time to arrive: a record of each for every warp.
@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP, DEEP>::kCtas)
 #pragma unroll
       for (int i = 0; i < W; ++i) {
         const bool keep = !__all_sync(0xffffffffu, paged_head_passes(tw[i], mw, log2_t, idle));
-        mw = keep ? fmaxf(mw, tw[i]) : mw;
+        mw = keep ? max_nan(mw, tw[i]) : mw;
         kept |= keep ? 1u << i : 0u;
       }
       a_prev[0] = a_prev[1] = 1.f;

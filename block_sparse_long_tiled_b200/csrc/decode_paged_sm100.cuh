@@ -129,9 +129,10 @@ __device__ __forceinline__ void paged_cluster_merge(const PagedDecodeParams& p,
       sum += w;
       o = fmaf(w, ld_cluster(o0 + i * 4, s), o);
     }
-    // Every split empty (a sequence of length 0): O = 0 and lse = -inf.
+    // Every split empty (a sequence of length 0): O = 0 and lse = -inf.  A split
+    // of NaN has a NaN lse, which the maximum drops and the sum keeps.
     p.o[head0 * D + i] = __float2bfloat16_rn(sum == 0.f ? 0.f : o / sum);
-    if (i % D == 0) p.lse[head0 + h] = mx == -INFINITY ? -INFINITY : mx + __logf(sum);
+    if (i % D == 0) p.lse[head0 + h] = sum == 0.f ? -INFINITY : mx + __logf(sum);
   }
   __syncwarp();
   cluster_sync();  // no CTA leaves while another may read its shared memory
@@ -188,7 +189,9 @@ __device__ __forceinline__ int paged_checked(const PagedRows& c, int page) {
 }
 
 // row_passes_log2 for a positive threshold, without its branches (only
-// (-inf) - (-inf) needs a word of its own).
+// (-inf) - (-inf) needs a word of its own).  The maxima come from max_nan: a tile
+// with a NaN score, or one behind it in its split, has a NaN here, is below no
+// border and is kept, so that the NaN reaches the outputs.
 __device__ __forceinline__ bool paged_head_passes(float local, float run, float log2_t, bool idle) {
   return idle | (local == -INFINITY) | (local - run < log2_t);
 }
@@ -502,12 +505,12 @@ __global__ void __launch_bounds__(kPgThreads, PagedCfg<D>::kCtas)
         scores(t, x);
         __syncwarp();
         if (lane == 0) mbar_arrive(kfree(s));
-        float top[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
+        float top[2] = {max_nan(x[0], x[2]), max_nan(x[1], x[3])};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1)
-            top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+            top[i] = max_nan(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
           if (g == 0) wmax[((t & 1) * 8 + 2 * c + i) * kPgWarps + warp] = top[i];
         }
       }
@@ -520,7 +523,7 @@ __global__ void __launch_bounds__(kPgThreads, PagedCfg<D>::kCtas)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float4 w = *reinterpret_cast<const float4*>(&wmax[((t & 1) * 8 + 2 * c + i) * kPgWarps]);
-          top[i] = fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w));
+          top[i] = max_nan(max_nan(w.x, w.y, w.z), w.w);
           pass &= paged_head_passes(top[i], m[i], log2_t, idle[i]);
         }
         keep = !__all_sync(0xffffffffu, pass);
@@ -535,7 +538,7 @@ __global__ void __launch_bounds__(kPgThreads, PagedCfg<D>::kCtas)
           }
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float mn = fmaxf(m[i], top[i]);
+            const float mn = max_nan(m[i], top[i]);
             na[i] = (m[i] == -INFINITY) ? 0.f : ex2_approx(m[i] - mn);
             m[i] = mn;
             l[i] *= na[i];
@@ -625,8 +628,9 @@ __global__ void __launch_bounds__(128) decode_paged_combine_kernel(const PagedDe
     w_s[lane + 32] = we;
     if (lane == 0) {
       sum_s = sum;
-      // Every split empty (a sequence of length 0): O = 0 and lse = -inf.
-      p.lse[bh] = mx == -INFINITY ? -INFINITY : mx + __logf(sum);
+      // Every split empty (a sequence of length 0): O = 0 and lse = -inf.  A split
+      // of NaN has a NaN lse, which the maximum drops and the sum keeps.
+      p.lse[bh] = sum == 0.f ? -INFINITY : mx + __logf(sum);
     }
   }
   __syncthreads();
