@@ -242,7 +242,8 @@ __device__ __forceinline__ void paged_merge_warps(const PagedDecodeParams& p, fl
     }
     const float lse = (mx + __log2f(sum)) * 0.69314718055994531f;
     if (p.S == 1) {
-      p.o[(head0 + h) * D + d] = __float2bfloat16_rn(o / sum);
+      // Scores that are all -inf: O = 0, as the merges of several splits leave it.
+      p.o[(head0 + h) * D + d] = __float2bfloat16_rn(sum == 0.f ? 0.f : o / sum);
       if (d == 0) p.lse[head0 + h] = lse;
     } else if (p.clustered) {
       part->o[h][d] = o / sum;

@@ -80,3 +80,19 @@ def test_every_key_of_nan(splits, fmt):
     assert np.isnan(got["o"][0]).all() and np.isnan(got["lse"][0]).all()
     assert np.isfinite(got["o"][1]).all() and np.isfinite(got["lse"][1]).all()
     assert got["count"][0] == int((got["tile_state"][1] == 2).sum())
+
+
+@pytest.mark.parametrize("tsf", [0.0, 3.0])
+@pytest.mark.parametrize("splits", [1, 4, 12])
+def test_scores_of_minus_infinity_alone_leave_nothing(splits, tsf):
+    """Keys whose scores are all -inf weigh nothing: O = 0 and lse = -inf for
+    every number of splits, as of a sequence without keys. (A 4-bit group
+    holds no infinity.)"""
+    c = Case([200, 130], tsf=tsf, splits=splits, planted=False, garbage=False)
+    c.q_t[0] = 1.0
+    for page in c.table[0, :-(-200 // c.P)]:
+        c.k_t[int(page)] = 1.0
+        c.k_t[int(page), :, :, 0] = float("-inf")
+    got = c.run()
+    assert np.all(got["o"][0] == 0) and np.all(got["lse"][0] == -np.inf)
+    assert np.isfinite(got["o"][1]).all() and np.isfinite(got["lse"][1]).all()
