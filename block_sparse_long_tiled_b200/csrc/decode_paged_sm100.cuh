@@ -12,7 +12,8 @@
 //   S^T[16 keys, 8 heads] = K Q^T,   O^T[d, 8 heads] += V^T P^T,
 // so eight heads fill the instruction (16-row query tiles would leave half of
 // it empty), and one 8x8 transpose of the packed P turns the first product's
-// result into the second's operand.  Each warp keeps O^T of its own keys in
+// result into the second's operand (P in two bf16 parts, so that it is as good
+// as the contiguous decode's, which holds it in fp32).  Each warp keeps O^T of its own keys in
 // registers; the warps merge once per split.  (tcgen05 has no use here: the
 // kernel is bound by HBM.)
 //
@@ -100,6 +101,11 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// What the rounding of a pair to bf16 left over, in bf16.
+__device__ __forceinline__ uint32_t pack_rest(float x, float y, uint32_t rounded) {
+  return pack_bf16x2(x - __uint_as_float(rounded << 16), y - __uint_as_float(rounded & 0xFFFF0000u));
 }
 
 // The splits of a head merged by the cluster they are, each CTA writing its
@@ -432,9 +438,13 @@ __global__ void __launch_bounds__(kPgThreads, PagedCfg<D>::kCtas)
               make_uint4(0, 0, 0, 0);
       __syncwarp();
     }
-    // P is rounded to bf16 for the product (2^-9 of each weight); l is not.
-    const uint32_t b0 = transpose8x8(pack_bf16x2(pr[0], pr[1]));
-    const uint32_t b1 = transpose8x8(pack_bf16x2(pr[2], pr[3]));
+    // P goes into the product as two bf16 parts, its rounding and the rest's
+    // (within 2^-16 of each weight): twice the products, in the shadow of HBM
+    // (64 x 16K-32K 896 us with one part or two, factor 500 647 and 650).
+    const uint32_t h0 = pack_bf16x2(pr[0], pr[1]), h1 = pack_bf16x2(pr[2], pr[3]);
+    const uint32_t b0 = transpose8x8(h0), b1 = transpose8x8(h1);
+    const uint32_t r0 = transpose8x8(pack_rest(pr[0], pr[1], h0));
+    const uint32_t r1 = transpose8x8(pack_rest(pr[2], pr[3], h1));
     const uint32_t base = smem_u32(tile) + warp * 16 * 128;
     const int row = (lane & 7) + (lane >> 4) * 8, ch = (lane >> 3) & 1;
 #pragma unroll
@@ -444,6 +454,7 @@ __global__ void __launch_bounds__(kPgThreads, PagedCfg<D>::kCtas)
       ldsm4_t(base + (chunk >> 3) * (kPgTile * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4),
               a);
       mma16816(acc[mt], a[0], a[1], a[2], a[3], b0, b1);
+      mma16816(acc[mt], a[0], a[1], a[2], a[3], r0, r1);
     }
   };
 

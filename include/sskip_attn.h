@@ -543,8 +543,9 @@ int sskip_kv_gather(const sskip_kv_gather_args* args, void* stream);
  *   skip_count: optional device uint64[2] = {skipped, visited} tiles.
  *   tile_state: optional [B, Hkv, ceil(max_pages * page_size / 64)] uint8:
  *     0 not visited, 1 kept, 2 skipped.
- * P is rounded to bf16 for its product with V, the row sum is not; in the
- * 4-bit form the value's scale joins P before that rounding.
+ * The row sum is fp32.  For its product with V, P is held to 2^-16 over bf16
+ * pages; over 4-bit pages, whose values are themselves rounded to a thirtieth of
+ * their group's spread, P (with the value's scale) is rounded to bf16.
  * SSKIP_KV_INT4 wants sm_scale <= 1e12 (SSKIP_ERR_UNSUPPORTED), |q| < 2^79 and
  * scales of values between 2^-41 and 2^71: beyond, results overflow, or values
  * below about 1e-12 lose precision.
