@@ -31,7 +31,8 @@ LIB_PATH = os.path.join(_PKG, "libsskip_attn.so")
 LIB_DEBUG_PATH = os.path.join(_PKG, "libsskip_attn_debug.so")
 
 EXPORTS = ("sskip_version", "sskip_status_string", "sskip_device_supported",
-           "sskip_attn_prefill", "sskip_attn_prefill_ex", "sskip_attn_prefill_vote",
+           "sskip_attn_prefill", "sskip_attn_prefill_ex", "sskip_attn_prefill_lens",
+           "sskip_attn_prefill_vote",
            "sskip_attn_decode_workspace_size",
            "sskip_attn_decode", "sskip_attn_decode_ex", "sskip_attn_decode_crit",
            "sskip_attn_decode_noalloc", "sskip_calibrate_factor", "sskip_hilbert3d_order",
@@ -98,6 +99,8 @@ def _load(path: str) -> ctypes.CDLL:
     L.sskip_attn_prefill.argtypes = pre + [P]
     L.sskip_attn_prefill_ex.restype = I
     L.sskip_attn_prefill_ex.argtypes = pre[:-1] + [P, P, P]
+    L.sskip_attn_prefill_lens.restype = I
+    L.sskip_attn_prefill_lens.argtypes = [P] + pre[:-1] + [P, P, P]
     L.sskip_attn_prefill_vote.restype = I
     L.sskip_attn_prefill_vote.argtypes = pre[:-1] + [I, P, P, P, P, P]
     L.sskip_attn_decode_workspace_size.restype = Z
@@ -223,6 +226,28 @@ def sskip_attn_prefill(q, k, v, o, lse, *, causal: bool, sm_scale: float,
                                      float(threshold_scale_factor), int(Br), int(Bc),
                                      _ptr(skip_count), _ptr(tile_state), _stream(stream))
     _check(rc, "sskip_attn_prefill")
+
+
+def sskip_attn_prefill_lens(q, k, v, seqlens, o, lse, *, causal: bool, sm_scale: float,
+                            threshold_scale_factor: float, Br: int = 128, Bc: int = 128,
+                            skip_count=None, tile_state=None, stream=None) -> None:
+    """sskip_attn_prefill of a padded batch: seqlens [B] int32 on the device are
+    its entries' own lengths (sskip_attn_prefill_lens)."""
+    for t in (q, k, v, o):
+        _bf16_view(t)
+    _dev(seqlens, torch.int32, "seqlens")
+    _dev(lse, torch.float32, "lse")
+    _dev(tile_state, torch.uint8, "tile_state")
+    _check_counts(skip_count, 2)
+    B, Hq, L, d = q.shape
+    Hkv = k.shape[1]
+    if seqlens.numel() != B:
+        raise ValueError(f"seqlens needs {B} entries")
+    rc = lib().sskip_attn_prefill_lens(_ptr(q), _ptr(k), _ptr(v), _ptr(seqlens), _ptr(o), _ptr(lse),
+                                       B, Hq, Hkv, L, d, int(bool(causal)), float(sm_scale),
+                                       float(threshold_scale_factor), int(Br), int(Bc),
+                                       _ptr(skip_count), _ptr(tile_state), _stream(stream))
+    _check(rc, "sskip_attn_prefill_lens")
 
 
 def sskip_attn_prefill_vote(q, k, v, o, lse, *, causal: bool, sm_scale: float,
@@ -390,10 +415,13 @@ def sskip_selftest_watchdog(limit_us: int, stream=None) -> None:
 # -------------------------------------------------------------- conveniences
 def prefill(q, k, v, *, causal: bool, sm_scale: float, threshold_scale_factor: float,
             Br: int = 128, Bc: int = 128, with_tiles: bool = False, vote_rows: int | None = None,
-            stream=None) -> dict:
+            seqlens=None, stream=None) -> dict:
     """Allocate outputs with torch and run sskip_attn_prefill on q's device;
     with ``vote_rows`` (Br or 32), run sskip_attn_prefill_vote instead and
-    also return the four counters and the slice record."""
+    also return the four counters and the slice record; with ``seqlens``, run
+    sskip_attn_prefill_lens."""
+    if seqlens is not None and vote_rows is not None:
+        raise ValueError("vote_rows and seqlens do not go together")
     B, Hq, L, d = q.shape
     rec_shape = (B, Hq, -(-L // Br), -(-L // Bc))
     with _alloc_on(stream):
@@ -403,6 +431,11 @@ def prefill(q, k, v, *, causal: bool, sm_scale: float, threshold_scale_factor: f
         counts = torch.zeros(2 if vote_rows is None else 4, dtype=torch.int64, device=q.device)
         smask = (torch.empty(rec_shape, dtype=torch.uint8, device=q.device)
                  if with_tiles and vote_rows is not None else None)
+    if seqlens is not None:
+        sskip_attn_prefill_lens(q, k, v, seqlens, o, lse, causal=causal, sm_scale=sm_scale,
+                                threshold_scale_factor=threshold_scale_factor, Br=Br, Bc=Bc,
+                                skip_count=counts, tile_state=tiles, stream=stream)
+        return {"o": o, "lse": lse, "counts": counts, "tile_state": tiles}
     if vote_rows is None:
         sskip_attn_prefill(q, k, v, o, lse, causal=causal, sm_scale=sm_scale,
                            threshold_scale_factor=threshold_scale_factor, Br=Br, Bc=Bc,
@@ -721,20 +754,24 @@ def prefill_paged(q, k, v, seq_ids, positions, k_pages, v_pages, block_table, *,
                   Br: int = 128, Bc: int = 128, stream=None) -> dict:
     """A batch of whole prompts of L tokens each, from projections q [B L,Hq,d],
     k, v [B L,Hkv,d]: append to the paged cache (norm, rotation) and causal
-    prefill of what was appended. A shorter prompt ends in padding (seq_ids < 0),
-    whose output rows mean nothing. Returns prefill's outputs."""
+    prefill of what was appended. A shorter prompt ends in padding (seq_ids < 0):
+    its rows, decisions and threshold are those of the prompt alone at its own
+    length, the rows of padding O = 0 and lse = -inf. Returns prefill's outputs."""
     T, Hq, d = q.shape
     Hkv = k.shape[1]
-    with _alloc_on(stream):  # rows of padding stay 0: their tile's other rows meet them
-        qr = torch.zeros((T // L, Hq, L, d), dtype=q.dtype, device=q.device)
-        kr, vr = (torch.zeros((T // L, Hkv, L, d), dtype=q.dtype, device=q.device)
-                  for _ in range(2))
+    with _alloc_on(stream):  # padding's rows are not written: those of v have to be finite
+        qr = torch.empty((T // L, Hq, L, d), dtype=q.dtype, device=q.device)
+        kr = torch.empty((T // L, Hkv, L, d), dtype=q.dtype, device=q.device)
+        vr = torch.zeros((T // L, Hkv, L, d), dtype=q.dtype, device=q.device)
     sskip_kv_append(q, k, v, seq_ids, positions, q_out=qr, k_out=kr, v_out=vr, k_pages=k_pages,
                     v_pages=v_pages, block_table=block_table, turns=turns, interleaved=interleaved,
                     attn_factor=attn_factor, q_weight=q_weight, k_weight=k_weight, eps=eps,
                     stream=stream)
+    with _alloc_on(stream):
+        lens = (seq_ids.view(-1, L) >= 0).sum(1, dtype=torch.int32)
     return prefill(qr, kr, vr, causal=True, sm_scale=sm_scale,
-                   threshold_scale_factor=threshold_scale_factor, Br=Br, Bc=Bc, stream=stream)
+                   threshold_scale_factor=threshold_scale_factor, Br=Br, Bc=Bc, seqlens=lens,
+                   stream=stream)
 
 
 def decode_step_paged(q, k, v, seq_ids, positions, seqlens, k_pages, v_pages, block_table, *,

@@ -62,6 +62,8 @@ struct PrefillParams {
   float scale_log2;            // sm_scale * log2(e)
   float log2_t;                // log2(tsf / L), -inf when tsf == 0
   int t_positive;
+  const int* seqlens;          // [B] (LENS): the rows of each batch entry
+  float tsf;                   // (LENS) t = tsf / seqlens[b]
 };
 
 constexpr int kPfThreads = 384;
@@ -137,6 +139,10 @@ struct PrefillCfg {
 // EXT = false compiles the plain block vote with the tile_state record only;
 // EXT = true adds the per-warp vote, the slice and critical-value records and
 // the four counters (kept out of the plain kernel, which they slow down).
+// LENS = true gives every batch entry its own length: its first seqlens[b] rows
+// are computed as a call with that L would (threshold, votes, tiles visited), the
+// rows behind them are O = 0 and lse = -inf.  A variant of its own, so that the
+// plain kernel keeps its length in the parameters.
 //
 // A kept tile's P (bf16) is stored over the first Bc/2 of its S columns in
 // two halves of Bc/2 keys, and P.V runs as two matching halves:
@@ -147,7 +153,7 @@ struct PrefillCfg {
 // never overwrites a P that P.V still reads, and its commit makes S(j+1) and
 // O visible together.  A skipped tile releases its S columns at the vote and
 // the next S follows at once.
-template <int D, int BR, int BC, bool CAUSAL, bool EXT>
+template <int D, int BR, int BC, bool CAUSAL, bool EXT, bool LENS>
 __global__ void __launch_bounds__(kPfThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const PrefillParams p) {
@@ -160,6 +166,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   constexpr uint32_t IDESC_S = idesc_bf16_f32(128, BC, 0, 0);
   constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, 0, 1);
   static_assert(BR == 64 || BR == 128, "Br");
+  static_assert(!(EXT && LENS), "the records have one length");
   static_assert(BC == 64 || BC == 128, "Bc");
 
   extern __shared__ uint8_t smem_raw[];
@@ -218,14 +225,39 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   const int hq = kvh * p.G + (rem - ublk * p.G);
   const int row0 = iu * kPfUnitRows;
 
+  // Rows, query tiles and key tiles of this batch entry; the strides of the
+  // tensors and records are p.L, p.n_q and p.n_k.
+  int L = p.L, n_q = p.n_q, n_k = p.n_k;
+  if constexpr (LENS) {
+    const int raw = p.seqlens[b];
+    if ((raw < 0 || raw > p.L) && rem == 0 && threadIdx.x == 0) latch_status(kStatusInvalidArg);
+    L = min(max(raw, 0), p.L);
+    n_q = (L + BR - 1) / BR;
+    n_k = (L + BC - 1) / BC;
+  }
+  auto empty_row = [&](int row) {  // behind the entry's last one
+    const size_t at = ((size_t)b * p.Hq + hq) * p.L + row;
+    uint4* dst = reinterpret_cast<uint4*>(p.o + at * D);
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+    p.lse[at] = -INFINITY;
+  };
+  if constexpr (LENS) {
+    if (row0 >= L) {  // (every thread: all return together)
+      const int row = row0 + (int)threadIdx.x;
+      if ((int)threadIdx.x < kPfUnitRows && row < p.L) empty_row(row);
+      return;
+    }
+  }
+
   // Key tiles each MMA tile visits (the union over its vote groups).
   auto tiles_visited = [&](int w) {
     int n = 0;
 #pragma unroll
     for (int g = 0; g < NGRP; ++g) {
       const int it = (row0 + 128 * w) / BR + g;
-      if (it < p.n_q) {
-        const int jm = CAUSAL ? min(p.n_k - 1, ((it + 1) * BR - 1) / BC) : p.n_k - 1;
+      if (it < n_q) {
+        const int jm = CAUSAL ? min(n_k - 1, ((it + 1) * BR - 1) / BC) : n_k - 1;
         n = max(n, jm + 1);
       }
     }
@@ -235,8 +267,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   const int n_j = max(n_a, n_b);
   // (Every thread computes the same unit, so all return together, before
   // any barrier.)
-  if (!dev_check(b < p.B && hq < p.Hq && kvh < p.Hkv && iu < p.n_units && row0 < p.L &&
-                 n_j <= p.n_k))
+  if (!dev_check(b < p.B && hq < p.Hq && kvh < p.Hkv && iu < p.n_units && row0 < L &&
+                 n_j <= n_k))
     return;
   static_assert(C::kOCol + 2 * D <= C::kTmemCols, "TMEM columns");
 
@@ -291,7 +323,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             if (okv && j - VS < n_w[w]) okv = mbar_wait(b_vread(w, j), vote_par(j) ^ 1u, abort_flag);
           if (!okv) break;
         }
-        if (!dev_check(j < p.n_k && b * p.Hkv + kvh < p.B * p.Hkv)) {
+        if (!dev_check(j < n_k && b * p.Hkv + kvh < p.B * p.Hkv)) {
           mbar_arrive(b_kfull(s));  // the phase completes without data
           continue;
         }
@@ -459,12 +491,12 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               bits |= fl[g * WPG + q] != 0 ? (1u << q) : 0u;
             }
             const int it = (row0 + 128 * w) / BR + g;  // this group's query tile
-            if (it >= p.n_q) continue;
-            const int jm = CAUSAL ? min(p.n_k - 1, ((it + 1) * BR - 1) / BC) : p.n_k - 1;
+            if (it >= n_q) continue;
+            const int jm = CAUSAL ? min(n_k - 1, ((it + 1) * BR - 1) / BC) : n_k - 1;
             if (j > jm) continue;  // the group does not visit tile j
             kept = kept || !all;
             const size_t rec = (((size_t)b * p.Hq + hq) * p.n_q + it) * p.n_k + j;
-            if (!dev_check(j < p.n_k && rec < (size_t)p.B * p.Hq * p.n_q * p.n_k)) continue;
+            if (!dev_check(j < n_k && rec < (size_t)p.B * p.Hq * p.n_q * p.n_k)) continue;
             ++n_vis;
             n_skip += all ? 1 : 0;
             if (p.tile_state) p.tile_state[rec] = all ? 2 : 1;
@@ -476,7 +508,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           if (kept && !issued) {
             const int vs = kc % NV;
             if (kc >= NV && !mbar_wait(b_vempty(vs), ((kc / NV) - 1) & 1, abort_flag)) break;
-            if (!dev_check(j < p.n_k && vs < NV)) {
+            if (!dev_check(j < n_k && vs < NV)) {
               mbar_arrive(b_vfull(vs));  // the phase completes without data
             } else {
               mbar_arrive_expect_tx(b_vfull(vs), C::kKVBytes);
@@ -512,15 +544,19 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     const int r = wq * 32 + lane;    // row within the 128-row tile
     const int grp = r / BR;
     const int row = row0 + 128 * wg + r;
-    const bool row_in = row < p.L;
+    const bool row_in = row < L;
+    // The first key that the row does not see: one number to mask by, not L and
+    // the row (16K causal, d = 128: 2001 us with two, 1970 with one; with LENS,
+    // where L is a register, 2083 and 2011).
+    const int end = CAUSAL ? min(L, row + 1) : L;
     const uint32_t lane_base = uint32_t(wq * 32) << 16;
     const uint32_t tO = tmem + C::kOCol + wg * D + lane_base;
     const int n_own = wg == 0 ? n_a : n_b;
     // Last key tile this row's vote group visits (-1: the group is padding).
     const int my_tile = (row0 + 128 * wg) / BR + grp;
-    const int my_jmax = my_tile >= p.n_q ? -1
-                        : CAUSAL ? min(p.n_k - 1, ((my_tile + 1) * BR - 1) / BC) : p.n_k - 1;
-    const float log2_t = p.log2_t;
+    const int my_jmax = my_tile >= n_q ? -1
+                        : CAUSAL ? min(n_k - 1, ((my_tile + 1) * BR - 1) / BC) : n_k - 1;
+    const float log2_t = LENS ? (float)log2((double)p.tsf / (double)L) : p.log2_t;
     const bool t_pos = p.t_positive != 0;
     const float scale = p.scale_log2;
 
@@ -550,14 +586,14 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       else tmem_wait_ld_tie64(sr);
       float* s = reinterpret_cast<float*>(sr);
 
-      // Mask: keys past L, and keys after the row in causal attention.
+      // Mask: keys past the length, and keys after the row in causal attention.
       const int key0 = j * BC;
-      const bool need_mask = (key0 + BC > p.L) || (CAUSAL && key0 + BC - 1 > row);
+      const bool need_mask = key0 + BC > end;
       if (need_mask) {
 #pragma unroll
         for (int c = 0; c < BC; ++c) {
           const int key = key0 + c;
-          if (key >= p.L || (CAUSAL && key > row)) s[c] = -INFINITY;
+          if (key >= end) s[c] = -INFINITY;
         }
       }
       // Three-input max tree: a first level of independent maxima over column
@@ -613,7 +649,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         for (int q = 0; q < WPG; ++q) grp_kept = grp_kept || fl[grp * WPG + q] == 0;
       }
       // Slice counters: warps holding at least one valid row of a visiting group.
-      if (EXT && lane == 0 && gvis && row0 + 128 * wg + wq * 32 < p.L) {
+      if (EXT && lane == 0 && gvis && row0 + 128 * wg + wq * 32 < L) {
         ++n_svis;
         n_sskip += wall ? 1 : 0;
       }
@@ -720,7 +756,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 #pragma unroll
           for (int c = 0; c < HK; ++c) {
             const int key = key0 + HK + c;
-            if (key >= p.L || (CAUSAL && key > row)) rr[c] = __float_as_uint(-INFINITY);
+            if (key >= end) rr[c] = __float_as_uint(-INFINITY);
           }
         }
         exp_half(1, reinterpret_cast<const float*>(rr));
@@ -758,7 +794,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     tc_fence_after();
     __syncwarp();
     const bool store = row_in && my_jmax >= 0 && n_own > 0 && l_run > 0.f &&
-                       dev_check(row < p.L && hq < p.Hq);
+                       dev_check(row < L && hq < p.Hq);
     if (n_own > 0) {
       const float inv_l = store ? 1.f / (SSKIP_PF_ROUNDED_L ? lr_run : l_run) : 0.f;
       __nv_bfloat16* orow = p.o + (((size_t)b * p.Hq + hq) * p.L + (store ? row : 0)) * D;
@@ -781,6 +817,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     if (store)
       p.lse[((size_t)b * p.Hq + hq) * p.L + row] =
           (m_ref - kPackBias + __log2f(l_run)) * 0.69314718055994531f;
+    if (LENS && !row_in && row < p.L) empty_row(row);
     if (EXT && lane == 0 && p.counts && p.n_counts == 4 && p.slice_vote && n_svis > 0) {
       atomicAdd(&p.counts[2], (unsigned long long)n_sskip);
       atomicAdd(&p.counts[3], (unsigned long long)n_svis);

@@ -94,10 +94,10 @@ cudaError_t ensure_smem(const void* kernel, int bytes) {
   return e;
 }
 
-template <int D, int BR, int BC, bool CAUSAL, bool EXT>
+template <int D, int BR, int BC, bool CAUSAL, bool EXT, bool LENS>
 int launch_prefill_t(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                      const PrefillParams& p, cudaStream_t st) {
-  auto kernel = prefill_kernel<D, BR, BC, CAUSAL, EXT>;
+  auto kernel = prefill_kernel<D, BR, BC, CAUSAL, EXT, LENS>;
   const int smem = PrefillCfg<D, BC>::kAlloc;
   if (ensure_smem(reinterpret_cast<const void*>(kernel), smem) != cudaSuccess)
     return SSKIP_ERR_CUDA;
@@ -123,8 +123,9 @@ template <int D, int BR, int BC, bool CAUSAL>
 int launch_prefill(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
                    const PrefillParams& p, cudaStream_t st) {
   const bool ext = p.slice_vote || p.slice_mask || p.tile_crit || p.n_counts == 4;
-  return ext ? launch_prefill_t<D, BR, BC, CAUSAL, true>(mq, mk, mv, p, st)
-             : launch_prefill_t<D, BR, BC, CAUSAL, false>(mq, mk, mv, p, st);
+  if (p.seqlens) return launch_prefill_t<D, BR, BC, CAUSAL, false, true>(mq, mk, mv, p, st);
+  return ext ? launch_prefill_t<D, BR, BC, CAUSAL, true, false>(mq, mk, mv, p, st)
+             : launch_prefill_t<D, BR, BC, CAUSAL, false, false>(mq, mk, mv, p, st);
 }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -185,7 +186,7 @@ int prefill_impl(const void* q, const void* k, const void* v, void* o, float* ls
                  int Hkv, int L, int d, int causal, float sm_scale, float threshold_scale_factor,
                  int Br, int Bc, int vote_rows, unsigned long long* counts, int n_counts,
                  uint8_t* tile_state, uint8_t* slice_mask, float* tile_crit, void* stream,
-                 bool zero_counts = true) {
+                 bool zero_counts = true, const int* seqlens = nullptr) {
   const int rc = prefill_check(q, k, v, o, lse, B, Hq, Hkv, L, d, sm_scale,
                                threshold_scale_factor, Br, Bc, vote_rows, counts, tile_crit);
   if (rc != SSKIP_OK) return rc;
@@ -216,6 +217,8 @@ int prefill_impl(const void* q, const void* k, const void* v, void* o, float* ls
   p.t_positive = threshold_scale_factor > 0.f;
   p.log2_t = p.t_positive ? (float)std::log2((double)threshold_scale_factor / (double)L)
                           : -INFINITY;
+  p.seqlens = seqlens;
+  p.tsf = threshold_scale_factor;
 
   if (counts && zero_counts &&
       cudaMemsetAsync(counts, 0, (size_t)n_counts * sizeof(unsigned long long), st) != cudaSuccess)
@@ -252,6 +255,18 @@ SSKIP_API int sskip_attn_prefill_ex(const void* q, const void* k, const void* v,
                                     void* stream) {
   return prefill_impl(q, k, v, o, lse, B, Hq, Hkv, L, d, causal, sm_scale, threshold_scale_factor,
                       Br, Bc, Br, skip_count, 2, tile_state, nullptr, nullptr, stream);
+}
+
+SSKIP_API int sskip_attn_prefill_lens(const void* q, const void* k, const void* v,
+                                      const int* seqlens, void* o, float* lse, int B, int Hq,
+                                      int Hkv, int L, int d, int causal, float sm_scale,
+                                      float threshold_scale_factor, int Br, int Bc,
+                                      unsigned long long* skip_count, uint8_t* tile_state,
+                                      void* stream) {
+  if (!seqlens || (reinterpret_cast<uintptr_t>(seqlens) & 3u)) return SSKIP_ERR_INVALID_ARG;
+  return prefill_impl(q, k, v, o, lse, B, Hq, Hkv, L, d, causal, sm_scale, threshold_scale_factor,
+                      Br, Bc, Br, skip_count, 2, tile_state, nullptr, nullptr, stream, true,
+                      seqlens);
 }
 
 SSKIP_API int sskip_attn_prefill_vote(const void* q, const void* k, const void* v, void* o,

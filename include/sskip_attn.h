@@ -112,6 +112,22 @@ int sskip_attn_prefill_ex(const void* q, const void* k, const void* v, void* o, 
                           unsigned long long* skip_count, uint8_t* tile_state, void* stream);
 
 /*
+ * Prefill of a batch whose entries have lengths of their own, padded to L:
+ * seqlens [B] int32 on the device, 0 <= seqlens[b] <= L.  The first seqlens[b]
+ * rows of entry b are those of sskip_attn_prefill_ex on that entry alone with
+ * L = seqlens[b]: t_b = threshold_scale_factor / seqlens[b], rows behind the end
+ * have no vote, tiles behind it are not visited and not counted.  The rows behind
+ * it are written O = 0 and lse = -inf.  tile_state keeps the shape of L.
+ * Another length is latched (SSKIP_ERR_INVALID_ARG) and clamped, as in
+ * sskip_attn_decode.  Rows of q and k behind the end may hold anything; those of
+ * v must be finite (they are multiplied by a probability of 0).
+ */
+int sskip_attn_prefill_lens(const void* q, const void* k, const void* v, const int* seqlens,
+                            void* o, float* lse, int B, int Hq, int Hkv, int L, int d, int causal,
+                            float sm_scale, float threshold_scale_factor, int Br, int Bc,
+                            unsigned long long* skip_count, uint8_t* tile_state, void* stream);
+
+/*
  * Prefill with a choice of vote granularity.  vote_rows = Br is the block
  * vote of sskip_attn_prefill.  vote_rows = 32 takes the same test per warp
  * slice of 32 query rows, the granularity of the "稀疏 Warp 在线 Softmax"
@@ -571,7 +587,7 @@ int sskip_attn_decode_paged(const sskip_decode_paged_args* args, void* stream);
  * word: SSKIP_OK, or the first device-side error latched since the last call
  * (SSKIP_ERR_TIMEOUT when a bounded wait inside a kernel ran out: the kernel
  * then abandoned its work, waited out its own copies in flight and left its
- * outputs undefined; SSKIP_ERR_INVALID_ARG when a decode length, a permute
+ * outputs undefined; SSKIP_ERR_INVALID_ARG when a sequence's length, a permute
  * index, or a sequence, position or page of the paged cache held in device
  * memory was out of range).  Returns SSKIP_ERR_CUDA if
  * the synchronisation itself failed.
