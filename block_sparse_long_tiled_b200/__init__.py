@@ -2,8 +2,8 @@
 
 Thin Python binding of libsskip_attn.so (C ABI in include/sskip_attn.h). The
 sskip_* functions below only marshal torch tensors into the C calls of the
-same names (those of the paged cache through the compiled _binding.so), and the conveniences after them only allocate outputs and chain
-those calls: every step of the computation runs in the library, in its CUDA
+same names (those of the paged cache through the compiled _binding*.so), and the
+conveniences after them only allocate outputs and chain those calls: every step of the computation runs in the library, in its CUDA
 kernels or, for the host-side steps (the calibration's factor selection, the
 Hilbert order and the rotation frequencies), in its C++. There is no CPU fallback; a missing
 library is an error.
@@ -18,8 +18,9 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
-import importlib
+import importlib.util
 import os
+import sys
 
 import torch
 
@@ -636,14 +637,24 @@ def sskip_rope_freqs(rot_dim: int, base: float, *, scaling: str = "plain", facto
     return turns, attn.value
 
 
+def binding_path() -> str:
+    """The compiled binding of this Python and this torch: it reads their
+    objects, so one that was built for others is another file."""
+    return os.path.join(_PKG, f"_binding_{sys.implementation.cache_tag}_torch{torch.__version__}.so")
+
+
 def _marshal():
     """The compiled marshalling of the paged-cache calls (csrc/binding.cpp)."""
     global _binding_module
     if _binding_module is None:
-        if not os.path.exists(os.path.join(_PKG, "_binding.so")):
-            raise RuntimeError(f"{_PKG}/_binding.so is missing: build it with "
+        path = binding_path()
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with "
                                "`python -m block_sparse_long_tiled_b200.build`")
-        _binding_module = importlib.import_module(__name__ + "._binding")
+        spec = importlib.util.spec_from_file_location(__name__ + "._binding", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _binding_module = module
     return _binding_module
 
 

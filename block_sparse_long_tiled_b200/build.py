@@ -1,6 +1,7 @@
 """Build libsskip_attn.so (release) and libsskip_attn_debug.so (device-side
-index checks, SSKIP_DEBUG_CHECKS=1) in-tree with nvcc for sm_100a, and
-_binding.so (the tensor marshalling of the paged-cache calls) with g++.
+index checks, SSKIP_DEBUG_CHECKS=1) in-tree with nvcc for sm_100a, and the
+binding of this Python and torch (the tensor marshalling of the paged-cache
+calls, _binding_<python>_torch<version>.so) with g++.
 
     python -m block_sparse_long_tiled_b200.build [--force]
 """
@@ -12,12 +13,13 @@ import subprocess
 import sys
 import sysconfig
 
+from block_sparse_long_tiled_b200 import binding_path
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libsskip_attn.so")
 LIB_DEBUG = os.path.join(PKG, "libsskip_attn_debug.so")
-BINDING = os.path.join(PKG, "_binding.so")
 BINDING_SOURCES = [os.path.join(CSRC, "binding.cpp"), os.path.join(ROOT, "include", "sskip_attn.h")]
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
               "-Xcompiler", "-fPIC,-fvisibility=hidden", "-shared"]
@@ -64,12 +66,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
         jobs.append((subprocess.Popen(cmd), tmp, lib, cmd))
-    if force or _stale(BINDING, BINDING_SOURCES):
-        tmp = f"{BINDING}.tmp{os.getpid()}"
+    binding = binding_path()
+    if force or _stale(binding, BINDING_SOURCES):
+        tmp = f"{binding}.tmp{os.getpid()}"
         cmd = _binding_cmd(tmp)
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
-        jobs.append((subprocess.Popen(cmd), tmp, BINDING, cmd))
+        jobs.append((subprocess.Popen(cmd), tmp, binding, cmd))
     for proc, tmp, lib, cmd in jobs:
         if proc.wait() != 0:
             raise subprocess.CalledProcessError(proc.returncode, cmd)
