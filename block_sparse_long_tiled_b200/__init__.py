@@ -664,7 +664,7 @@ def _paged_call(name: str, t, stream, *args) -> None:
     for the length of the call."""
     L = lib()
     address, marshal = L.paged_addresses[name], getattr(_marshal(), _PAGED[name])
-    dev = t.get_device()
+    dev = t.get_device() if isinstance(t, torch.Tensor) else -1  # which the binding refuses by name
     if stream is None:
         stream = torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else 0
     elif hasattr(stream, "cuda_stream"):
@@ -733,7 +733,7 @@ def paged_cache(num_pages: int, Hkv: int, page_size: int, d: int, *, int4: bool 
 def paged_splits(B: int, Hkv: int, max_len: int) -> int:
     """A num_splits that gives every SM four CTAs where the sequences are long
     enough (a split has at least four tiles of 64 keys)."""
-    return max(1, min(64, -(-592 // (B * Hkv)), -(-max_len // 256)))
+    return max(1, min(64, -(-592 // max(1, B * Hkv)), -(-max_len // 256)))
 
 
 def decode_paged(q, k_pages, v_pages, block_table, seqlens, *, sm_scale: float,

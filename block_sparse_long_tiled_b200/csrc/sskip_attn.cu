@@ -830,10 +830,31 @@ int kv_warps_per_token(int T, int units, int heads_per_warp) {
   return (int)std::min<long long>(most, std::max<long long>(1, 148ll * 64 / T));
 }
 
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && x < y + nb && y < x + na;
+// Memory that a call reads or (out) writes.
+struct Range {
+  const void* p;
+  size_t n;
+  bool out;
+};
+
+// Rows are written while others are still read: no output may share memory with
+// an input or another output.
+template <size_t N>
+bool outputs_overlap(const Range (&r)[N]) {
+  for (size_t i = 0; i < N; ++i)
+    for (size_t j = i + 1; j < N; ++j) {
+      if (!(r[i].out || r[j].out) || !r[i].p || !r[j].p || !r[i].n || !r[j].n) continue;
+      const uintptr_t x = reinterpret_cast<uintptr_t>(r[i].p), y = reinterpret_cast<uintptr_t>(r[j].p);
+      if (x < y + r[j].n && y < x + r[i].n) return true;
+    }
+  return false;
 }
+
+// A call's pages (one pool's bytes) and its block table's.
+size_t pool_bytes(const sskip_paged_cache& c, int Hkv, int d) {
+  return c.num_pages * sskip_kv_page_bytes(c.kv_format, Hkv, c.page_size, d);
+}
+size_t table_bytes(const sskip_paged_cache& c) { return (size_t)c.B * c.max_pages * 4; }
 
 // 2-D bf16 map over the rows of every page and head, box {64, box_rows},
 // 128-byte swizzle.
@@ -1006,23 +1027,19 @@ SSKIP_API int sskip_kv_append(const sskip_kv_append_args* args, void* stream) {
   }
   const int units = Hq + 2 * Hkv, heads = 32 / (d / 16);
   if (units > (1 << 20)) return SSKIP_ERR_UNSUPPORTED;
-  // Rows are written while others are still read: no output may share memory
-  // with an input or another output.
   {
-    struct Range { const void* p; size_t n; bool out; };
     const size_t qn = (size_t)T * Hq * d * 2, kn = (size_t)T * Hkv * d * 2;
     auto span = [&](long long stride, int H) { return ((size_t)(T - 1) * stride + (size_t)H * d) * 2; };
-    const size_t pages =
-        cached ? a.cache.num_pages * sskip_kv_page_bytes(a.cache.kv_format, Hkv, a.cache.page_size, d)
-               : 0;
+    const size_t pages = cached ? pool_bytes(a.cache, Hkv, d) : 0;
     const Range r[] = {{q, Hq ? span(q_stride, Hq) : 0, false}, {k, Hkv ? span(k_stride, Hkv) : 0, false},
                        {v, Hkv ? span(v_stride, Hkv) : 0, false}, {q_out, qn, true},
                        {k_out, kn, true}, {v_out, kn, true}, {k_pages, pages, true},
-                       {v_pages, pages, true}};
-    for (int i = 0; i < 8; ++i)
-      for (int j = i + 1; j < 8; ++j)
-        if ((r[i].out || r[j].out) && overlap(r[i].p, r[i].n, r[j].p, r[j].n))
-          return SSKIP_ERR_INVALID_ARG;
+                       {v_pages, pages, true}, {seq_ids, (size_t)T * 4, false},
+                       {positions, (size_t)T * 4, false}, {q_weight, (size_t)d * 2, false},
+                       {k_weight, (size_t)d * 2, false}, {turns, (size_t)rot_dim * 4, false},
+                       {cached ? a.cache.block_table : nullptr, cached ? table_bytes(a.cache) : 0,
+                        false}};
+    if (outputs_overlap(r)) return SSKIP_ERR_INVALID_ARG;
   }
   AppendParams p{};
   p.q = static_cast<const __nv_bfloat16*>(q);
@@ -1084,11 +1101,12 @@ SSKIP_API int sskip_kv_gather(const sskip_kv_gather_args* args, void* stream) {
   const long long warps = (long long)T * wpt;
   if (warps > 0x7FFFFFFFll - 8 || Hkv > (1 << 19)) return SSKIP_ERR_UNSUPPORTED;
   const size_t on = (size_t)T * Hkv * d * 2;
-  const size_t pages = a.cache.num_pages * sskip_kv_page_bytes(kv_format, Hkv, a.cache.page_size, d);
-  if (overlap(k_out, on, v_out, on) || overlap(k_out, on, k_pages, pages) ||
-      overlap(k_out, on, v_pages, pages) || overlap(v_out, on, k_pages, pages) ||
-      overlap(v_out, on, v_pages, pages))
-    return SSKIP_ERR_INVALID_ARG;
+  const size_t pages = pool_bytes(a.cache, Hkv, d);
+  const Range r[] = {{k_out, on, true}, {v_out, on, true}, {k_pages, pages, false},
+                     {v_pages, pages, false}, {seq_ids, (size_t)T * 4, false},
+                     {positions, (size_t)T * 4, false},
+                     {a.cache.block_table, table_bytes(a.cache), false}};
+  if (outputs_overlap(r)) return SSKIP_ERR_INVALID_ARG;
   GatherParams p{};
   p.seq_ids = seq_ids;
   p.positions = positions;
@@ -1137,19 +1155,16 @@ SSKIP_API int sskip_attn_decode_paged(const sskip_decode_paged_args* args, void*
   if (num_splits > 1 &&
       (!workspace || workspace_bytes < sskip_attn_decode_workspace_size(B, Hq, d, num_splits)))
     return SSKIP_ERR_INVALID_ARG;
-  // The CTAs of a call write while others still read.
   const size_t heads = (size_t)B * Hq;
-  const size_t pages = num_pages * sskip_kv_page_bytes(kv_format, Hkv, page_size, d);
-  const bool split = num_splits > 1;
-  const struct { const void* p; size_t n; } range[] = {
-      {o, heads * d * 2},
-      {lse, heads * 4},
-      {split ? workspace : nullptr,
-       split ? sskip_attn_decode_workspace_size(B, Hq, d, num_splits) : 0},
-      {q, heads * d * 2}, {k_pages, pages}, {v_pages, pages}};
-  for (int i = 0; i < 3; ++i)
-    for (int j = i + 1; j < 6; ++j)
-      if (overlap(range[i].p, range[i].n, range[j].p, range[j].n)) return SSKIP_ERR_INVALID_ARG;
+  const size_t pages = pool_bytes(a.cache, Hkv, d);
+  const size_t n_k_max = ((size_t)max_pages * page_size + kPgTile - 1) / kPgTile;
+  const size_t scratch = num_splits > 1 ? sskip_attn_decode_workspace_size(B, Hq, d, num_splits) : 0;
+  const Range r[] = {{o, heads * d * 2, true}, {lse, heads * 4, true}, {workspace, scratch, true},
+                     {skip_count, 16, true}, {tile_state, (size_t)B * Hkv * n_k_max, true},
+                     {q, heads * d * 2, false}, {k_pages, pages, false}, {v_pages, pages, false},
+                     {seqlens, (size_t)B * 4, false},
+                     {a.cache.block_table, table_bytes(a.cache), false}};
+  if (outputs_overlap(r)) return SSKIP_ERR_INVALID_ARG;
 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const size_t rows = (size_t)B * Hq * num_splits;
@@ -1166,7 +1181,7 @@ SSKIP_API int sskip_attn_decode_paged(const sskip_decode_paged_args* args, void*
   p.counts = skip_count;
   p.tile_state = tile_state;
   p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.G = G; p.S = num_splits;
-  p.n_k_max = (int)(((long long)max_pages * page_size + kPgTile - 1) / kPgTile);
+  p.n_k_max = (int)n_k_max;
   p.scale_log2 = (float)((double)sm_scale * 1.4426950408889634);
   p.tsf = threshold_scale_factor;
   // Up to eight splits whose CTAs all run at once merge in their cluster; a

@@ -503,8 +503,8 @@ int sskip_rope_freqs(int rot_dim, double base, int scaling, double factor, doubl
  *     at a time, may write the same position of a page.
  *
  * Norm and rotation run in fp32 with one rounding at the end, to bf16 or (for
- * SSKIP_KV_INT4) from fp32 to the 4-bit form.  No output may overlap an input
- * or another output.  T = 0 is a call that does nothing.
+ * SSKIP_KV_INT4) from fp32 to the 4-bit form.  No output may overlap an input,
+ * indices and tables among them, or another output.  T = 0 is a call that does nothing.
  */
 typedef struct {
     sskip_paged_cache cache;  /* k_pages = v_pages = NULL: no cache */
@@ -526,7 +526,8 @@ int sskip_kv_append(const sskip_kv_append_args* args, void* stream);
  * values into k_out, v_out [T / out_len, Hkv, out_len, d].  A cached prefix for
  * the prefill, a contiguous cache for sskip_attn_decode, an export.  4-bit
  * values are computed in fp32 and rounded once to bf16.  The same token may be
- * asked for several times.  T = 0 does nothing.
+ * asked for several times.  The outputs may not overlap each other or anything
+ * that the call reads.  T = 0 does nothing.
  */
 typedef struct {
     sskip_paged_cache cache;
@@ -545,8 +546,8 @@ int sskip_kv_gather(const sskip_kv_gather_args* args, void* stream);
  * in either format.
  *
  *   q [B, Hq, d], o [B, Hq, d] bf16, lse [B, Hq] fp32 natural log.
- *     No two of o, lse and the workspace, nor one of them and q or the pages,
- *     may overlap.
+ *     No output, the workspace, skip_count and tile_state among them, may
+ *     overlap another or anything that the call reads.
  *   seqlens [B] int32 on the device, 0 <= seqlens[b] <= max_pages * page_size.
  *     0 gives O = 0 and lse = -inf (a padded batch entry).  Another length is
  *     latched and clamped; a page outside the pool is latched and read as page
