@@ -270,11 +270,11 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm<D, G>())
         }
         const float dot = transpose_reduce8<G>(acc, sub);
         s[ps] = (key < keys) ? dot * p.scale_log2 : -INFINITY;
-        mx = fmaxf(mx, s[ps]);
+        mx = max_nan(mx, s[ps]);  // a tile with a NaN fails the vote and is kept
       }
       // per-head max over the warp's 4 key groups (lane bits 3, 4)
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+      mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+      mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
       if (kq == 0 && owner) wmax[((t & 1) * G + hs) * kDecWarps + warp] = mx;
     }
     __syncthreads();  // maxima of tile t published; K slot t % NK free; P.V of t-1-LAG done
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm<D, G>())
       const float* wm = wmax + ((t & 1) * G + hv) * kDecWarps;
       float m_loc = wm[0];
 #pragma unroll
-      for (int w = 1; w < kDecWarps; ++w) m_loc = fmaxf(m_loc, wm[w]);
+      for (int w = 1; w < kDecWarps; ++w) m_loc = max_nan(m_loc, wm[w]);
       const bool skip =
           __all_sync(0xffffffffu, row_passes_log2(m_loc, m_run, log2_t, t_positive));
       if (CRIT && warp == 0) {
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm<D, G>())
               gap * 0.69314718055994531f + logf((float)Lb);
       }
       if (!skip) {
-        const float m_new = fmaxf(m_run, m_loc);
+        const float m_new = max_nan(m_run, m_loc);
         const float a = (m_run == -INFINITY) ? 0.f : ex2_approx(m_run - m_new);
         m_run = m_new;
         const float mh = __shfl_sync(0xffffffffu, m_new, hs);  // lane hs holds head hs
@@ -453,10 +453,11 @@ __global__ void __launch_bounds__(128) decode_combine_kernel(const DecodeParams 
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     // Every split empty (a sequence of length 0, or aborted splits): O = 0
-    // and lse = -inf rather than 0 / 0.
-    if (threadIdx.x == 0) lse_s = sum > 0.f ? mx + __logf(sum) : -INFINITY;
+    // and lse = -inf rather than 0 / 0.  A split of NaN has a NaN lse, which the
+    // maximum drops and the sum keeps.
+    if (threadIdx.x == 0) lse_s = sum == 0.f ? -INFINITY : mx + __logf(sum);
     __syncwarp();
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     for (int s = threadIdx.x; s < p.S; s += 32) w_s[s] *= inv;
   }
   __syncthreads();
