@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     n_q = (L + BR - 1) / BR;
     n_k = (L + BC - 1) / BC;
   }
-  auto empty_row = [&](int row) {  // behind the entry's last one
+  auto empty_row = [&](int row) {  // nothing weighs: O = 0 and lse = -inf
     const size_t at = ((size_t)b * p.Hq + hq) * p.L + row;
     uint4* dst = reinterpret_cast<uint4*>(p.o + at * D);
 #pragma unroll
@@ -596,21 +596,22 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           if (key >= end) s[c] = -INFINITY;
         }
       }
-      // Three-input max tree: a first level of independent maxima over column
+      // A maximum that keeps a NaN: its row fails the vote, so that the tile is kept
+      // and the NaN reaches the outputs.  Three-input max tree: a first level of independent maxima over column
       // triples, then levels of three until one value is left.
       float t[(BC + 2) / 3];
 #pragma unroll
-      for (int i = 0; i < BC / 3; ++i) t[i] = fmax3(s[3 * i], s[3 * i + 1], s[3 * i + 2]);
+      for (int i = 0; i < BC / 3; ++i) t[i] = max_nan(s[3 * i], s[3 * i + 1], s[3 * i + 2]);
       int n = BC / 3;
       if (BC % 3 == 1) t[n++] = s[BC - 1];
-      if (BC % 3 == 2) t[n++] = fmaxf(s[BC - 2], s[BC - 1]);
+      if (BC % 3 == 2) t[n++] = max_nan(s[BC - 2], s[BC - 1]);
 #pragma unroll
       for (int level = 0; level < 5; ++level) {
         int m = 0;
 #pragma unroll
-        for (int i = 0; i + 2 < n; i += 3) t[m++] = fmax3(t[i], t[i + 1], t[i + 2]);
+        for (int i = 0; i + 2 < n; i += 3) t[m++] = max_nan(t[i], t[i + 1], t[i + 2]);
         if (n % 3 == 1) t[m++] = t[n - 1];
-        if (n % 3 == 2) t[m++] = fmaxf(t[n - 2], t[n - 1]);
+        if (n % 3 == 2) t[m++] = max_nan(t[n - 2], t[n - 1]);
         n = m;
       }
       const float m_loc = t[0] * scale;  // scale > 0
@@ -664,7 +665,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       float alpha = 1.f;
       bool rescale = false;
       if (mine) {
-        const float m_new = fmaxf(m_run, m_loc);
+        const float m_new = max_nan(m_run, m_loc);
         m_run = m_new;
         if (m_ref == -INFINITY) {
           m_ref = m_new;  // first kept tile of the row: its O row is still zero
@@ -793,7 +794,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     mbar_wait(b_mmadone, 0, abort_flag);
     tc_fence_after();
     __syncwarp();
-    const bool store = row_in && my_jmax >= 0 && n_own > 0 && l_run > 0.f &&
+    // (l_run = 0: scores that are all -inf, which weigh nothing, or a wait that
+    // gave up.  A NaN is stored.)
+    const bool store = row_in && my_jmax >= 0 && n_own > 0 && !(l_run <= 0.f) &&
                        dev_check(row < L && hq < p.Hq);
     if (n_own > 0) {
       const float inv_l = store ? 1.f / (SSKIP_PF_ROUNDED_L ? lr_run : l_run) : 0.f;
@@ -817,7 +820,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     if (store)
       p.lse[((size_t)b * p.Hq + hq) * p.L + row] =
           (m_ref - kPackBias + __log2f(l_run)) * 0.69314718055994531f;
-    if (LENS && !row_in && row < p.L) empty_row(row);
+    if (!store && row < p.L) empty_row(row);
     if (EXT && lane == 0 && p.counts && p.n_counts == 4 && p.slice_vote && n_svis > 0) {
       atomicAdd(&p.counts[2], (unsigned long long)n_sskip);
       atomicAdd(&p.counts[3], (unsigned long long)n_svis);

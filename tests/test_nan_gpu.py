@@ -1,5 +1,6 @@
-"""NaN scores in the contiguous decode: a NaN reaches the rows it belongs to
-and no other, whatever the threshold."""
+"""NaN and infinite scores in the prefill and the contiguous decode: a NaN
+reaches the rows it belongs to and no other, whatever the threshold; rows whose
+scores are all -inf give O = 0 and lse = -inf."""
 import pytest
 import torch
 
@@ -18,6 +19,79 @@ def _built():
 def inputs(B, Hq, Hkv, L, d, seed=1):
     g = torch.Generator(device="cuda").manual_seed(seed)
     return [torch.randn(B, h, L, d, device="cuda", generator=g).bfloat16() for h in (Hq, Hkv, Hkv)]
+
+
+def dirty(*shape):
+    """Memory that outputs may be allocated in holds numbers."""
+    for dtype in (torch.bfloat16, torch.float32):
+        x = torch.full(shape if dtype == torch.bfloat16 else shape[:-1], 3.0, device="cuda", dtype=dtype)
+        del x
+
+
+def call(form, q, k, v, **kw):
+    dirty(*q.shape)
+    if form == "lens":
+        kw["seqlens"] = torch.full((q.shape[0],), q.shape[2], dtype=torch.int32, device="cuda")
+    if form == "vote":
+        kw["vote_rows"] = 32
+    out = sk.prefill(q, k, v, sm_scale=q.shape[3] ** -0.5, **kw)
+    torch.cuda.synchronize()
+    assert sk.sskip_get_status() == sk.SSKIP_OK
+    return out["o"], out["lse"]
+
+
+FORM = pytest.mark.parametrize("form", ["plain", "lens", "vote"])
+SHAPE = pytest.mark.parametrize("L,d,tile", [(40, 128, 128), (300, 128, 128), (300, 64, 64), (130, 64, 128)])
+
+
+@FORM
+@SHAPE
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("tsf", [0.0, 3.0])
+def test_prefill_of_queries_of_nan(tsf, causal, L, d, tile, form):
+    q, k, v = inputs(2, 2, 1, L, d)
+    kw = dict(causal=causal, threshold_scale_factor=tsf, Br=tile, Bc=tile)
+    clean = call(form, q, k, v, **kw)
+    q[0, 0] = float("nan")       # a whole head
+    q[1, 1, 17] = float("nan")   # one row
+    o, lse = call(form, q, k, v, **kw)
+    assert bool(o[0, 0].isnan().all()) and bool(lse[0, 0].isnan().all())
+    assert bool(o[1, 1, 17].isnan().all()) and bool(lse[1, 1, 17].isnan())
+    o[0, 0], lse[0, 0] = clean[0][0, 0], clean[1][0, 0]
+    o[1, 1, 17], lse[1, 1, 17] = clean[0][1, 1, 17], clean[1][1, 1, 17]
+    assert bool(torch.isfinite(o.float()).all()) and bool(torch.isfinite(lse).all())
+    if tsf == 0:  # (with a threshold the row keeps tiles for its query tile)
+        assert torch.equal(o, clean[0]) and torch.equal(lse, clean[1])
+
+
+@FORM
+@SHAPE
+@pytest.mark.parametrize("tsf", [0.0, 3.0])
+@pytest.mark.parametrize("at", [0, 33])
+def test_prefill_of_a_key_of_nan(at, tsf, L, d, tile, form):
+    q, k, v = inputs(1, 2, 2, L, d)
+    kw = dict(causal=True, threshold_scale_factor=tsf, Br=tile, Bc=tile)
+    clean = call(form, q, k, v, **kw)
+    k[0, 0, at] = float("nan")
+    o, lse = call(form, q, k, v, **kw)
+    assert bool(o[0, 0, at:].isnan().all()) and bool(lse[0, 0, at:].isnan().all())
+    assert torch.equal(o[0, 1], clean[0][0, 1]) and torch.equal(lse[0, 1], clean[1][0, 1])
+    assert bool(torch.isfinite(o[0, 0, :at].float()).all())
+
+
+@FORM
+@SHAPE
+@pytest.mark.parametrize("tsf", [0.0, 3.0])
+def test_prefill_of_scores_of_minus_infinity(tsf, L, d, tile, form):
+    q, k, v = inputs(2, 2, 1, L, d)
+    kw = dict(causal=True, threshold_scale_factor=tsf, Br=tile, Bc=tile)
+    q[0], k[0] = 1.0, 1.0
+    k[0, :, :, 0] = float("-inf")
+    clean = call(form, q[1:], k[1:], v[1:], **kw)
+    o, lse = call(form, q, k, v, **kw)
+    if tsf > 0:  # every tile passes: nothing is weighed
+        assert bool((o[0] == 0).all()) and bool((lse[0] == -float("inf")).all())
+    assert torch.equal(o[1], clean[0][0]) and torch.equal(lse[1], clean[1][0])
 
 
 @pytest.mark.parametrize("tsf", [0.0, 3.0])
