@@ -679,7 +679,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       }
       // P = exp2(S * scale - m_ref) for kept rows, 0 otherwise; bf16 pairs.
       const uint64_t scale2 = f2pack(scale, scale);
-      const float nref = mine ? kPackBias - m_ref : -INFINITY;
+      // (m_ref is -inf while every score was: those weigh 0, not exp2(-inf + inf).)
+      const float nref = mine ? (m_ref == -INFINITY ? 0.f : kPackBias - m_ref) : -INFINITY;
       const uint64_t nref2 = f2pack(nref, nref);
       __syncwarp();
       if (__any_sync(0xffffffffu, rescale)) {

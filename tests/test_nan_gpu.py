@@ -89,9 +89,29 @@ def test_prefill_of_scores_of_minus_infinity(tsf, L, d, tile, form):
     k[0, :, :, 0] = float("-inf")
     clean = call(form, q[1:], k[1:], v[1:], **kw)
     o, lse = call(form, q, k, v, **kw)
-    if tsf > 0:  # every tile passes: nothing is weighed
-        assert bool((o[0] == 0).all()) and bool((lse[0] == -float("inf")).all())
+    assert bool((o[0] == 0).all()) and bool((lse[0] == -float("inf")).all())
     assert torch.equal(o[1], clean[0][0]) and torch.equal(lse[1], clean[1][0])
+
+
+@FORM
+@pytest.mark.parametrize("tsf", [0.0, 3.0])
+@pytest.mark.parametrize("d,tile", [(128, 128), (64, 64)])
+def test_prefill_behind_tiles_of_minus_infinity(d, tile, tsf, form):
+    """Keys of -inf scores at the front, a tile and more of them, leave the rows
+    what the other keys alone make of them (non-causal: those keys' own call)."""
+    q, k, v = inputs(1, 2, 1, 300, d)
+    q.clamp_(min=0.125)
+    k[:, :, :150] = float("-inf")
+    o, lse = call(form, q, k, v, causal=False, threshold_scale_factor=0.0, Br=tile, Bc=tile)
+    s = d ** -0.5 * q.double() @ k[:, :, 150:].double().transpose(2, 3)
+    want = s.softmax(-1) @ v[:, :, 150:].double()
+    # P in bf16 and O's own rounding: half a step each of o and of sum P |v|
+    tol = 2.0 ** -7 * (want.abs() + s.softmax(-1) @ v[:, :, 150:].double().abs())
+    assert bool(((o.double() - want).abs() <= tol).all())
+    assert float((lse.double() - s.logsumexp(-1)).abs().max()) < 1e-3
+    o, lse = call(form, q, k, v, causal=True, threshold_scale_factor=tsf, Br=tile, Bc=tile)
+    assert bool((o[:, :, :150] == 0).all()) and bool((lse[:, :, :150] == -float("inf")).all())
+    assert bool(torch.isfinite(o.float()).all()) and bool(torch.isfinite(lse[:, :, 150:]).all())
 
 
 @pytest.mark.parametrize("tsf", [0.0, 3.0])
