@@ -303,7 +303,9 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm<D, G>())
         const float m_new = max_nan(m_run, m_loc);
         const float a = (m_run == -INFINITY) ? 0.f : ex2_approx(m_run - m_new);
         m_run = m_new;
-        const float mh = __shfl_sync(0xffffffffu, m_new, hs);  // lane hs holds head hs
+        // Lane hs holds head hs.  (The maximum is -inf while every score was: those
+        // weigh 0, not exp2(-inf + inf).)
+        const float mh = __shfl_sync(0xffffffffu, m_new == -INFINITY ? 0.f : m_new, hs);
         const float ah = __shfl_sync(0xffffffffu, a, hs);
         const float p0 = ex2_approx(s[0] - mh), p1 = ex2_approx(s[1] - mh);
         l_lane = ah * l_lane + p0 + p1;

@@ -116,6 +116,31 @@ def test_prefill_behind_tiles_of_minus_infinity(d, tile, tsf, form):
 
 @pytest.mark.parametrize("tsf", [0.0, 3.0])
 @pytest.mark.parametrize("splits", [1, 4, 12])
+@pytest.mark.parametrize("paged", [False, True])
+def test_decode_behind_tiles_of_minus_infinity(paged, splits, tsf):
+    lens = torch.tensor([700, 130], dtype=torch.int32, device="cuda")
+    _, k, v = inputs(2, 4, 2, 704, 128)
+    q = torch.rand(2, 4, 128, device="cuda", generator=torch.Generator("cuda").manual_seed(2)).bfloat16()
+    k[:, :, :130] = float("-inf")
+    kw = dict(sm_scale=128 ** -0.5, threshold_scale_factor=tsf, num_splits=splits)
+    if paged:
+        pages = [x.unflatten(2, (11, 64)).transpose(1, 2).flatten(0, 1).contiguous() for x in (k, v)]
+        table = torch.arange(22, device="cuda", dtype=torch.int32).view(2, 11)
+        got = sk.decode_paged(q, *pages, table, lens, **kw)
+    else:
+        got = sk.decode(q, k, v, lens, **kw)
+    torch.cuda.synchronize()
+    assert bool((got["o"][1] == 0).all()) and bool((got["lse"][1] == -float("inf")).all())
+    assert bool(torch.isfinite(got["o"][0].float()).all()) and bool(torch.isfinite(got["lse"][0]).all())
+    if tsf == 0:
+        s = 128 ** -0.5 * torch.einsum("hgd,hnd->hgn", q[0].double().unflatten(0, (2, 2)), k[0, :, 130:700].double())
+        want = torch.einsum("hgn,hnd->hgd", s.softmax(-1), v[0, :, 130:700].double()).flatten(0, 1)
+        assert float((got["o"][0].double() - want).abs().max()) < 4e-3  # half a step below 1, and more
+        assert float((got["lse"][0].double() - s.logsumexp(-1).flatten()).abs().max()) < 1e-3
+
+
+@pytest.mark.parametrize("tsf", [0.0, 3.0])
+@pytest.mark.parametrize("splits", [1, 4, 12])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("Hq", [2, 8])
 def test_contiguous_decode_of_nan(Hq, d, splits, tsf):
