@@ -778,11 +778,12 @@ def prefill_paged(q, k, v, seq_ids, positions, k_pages, v_pages, block_table, *,
                     v_pages=v_pages, block_table=block_table, turns=turns, interleaved=interleaved,
                     attn_factor=attn_factor, q_weight=q_weight, k_weight=k_weight, eps=eps,
                     stream=stream)
-    with _alloc_on(stream):
-        lens = (seq_ids.view(-1, L) >= 0).sum(1, dtype=torch.int32)
-    return prefill(qr, kr, vr, causal=True, sm_scale=sm_scale,
-                   threshold_scale_factor=threshold_scale_factor, Br=Br, Bc=Bc, seqlens=lens,
-                   stream=stream)
+    with torch.cuda.device(q.device):  # which the prefill takes for current
+        with _alloc_on(stream):
+            lens = (seq_ids.view(-1, L) >= 0).sum(1, dtype=torch.int32)
+        return prefill(qr, kr, vr, causal=True, sm_scale=sm_scale,
+                       threshold_scale_factor=threshold_scale_factor, Br=Br, Bc=Bc, seqlens=lens,
+                       stream=stream)
 
 
 def decode_step_paged(q, k, v, seq_ids, positions, seqlens, k_pages, v_pages, block_table, *,

@@ -170,3 +170,29 @@ def test_a_prompt_does_not_depend_on_its_batch(tsf, int4):
         counts += one["counts"]
     assert torch.equal(got["counts"], counts)
     assert sk.sskip_get_status() == sk.SSKIP_OK
+
+
+@gpu
+def test_prefill_paged_makes_its_tensors_device_current(monkeypatch):
+    """The prefill runs on the current device's stream: prefill_paged makes that
+    of its tensors current, as the append and the decode do by themselves."""
+    entered, seen = [], []
+    real, prefill = torch.cuda.device, sk.prefill
+
+    class Guard(real):
+        def __enter__(self):
+            entered.append(self.idx)
+            return super().__enter__()
+
+        def __exit__(self, *a):
+            entered.pop()
+            return super().__exit__(*a)
+
+    monkeypatch.setattr(torch.cuda, "device", Guard)
+    monkeypatch.setattr(sk, "prefill", lambda *a, **kw: (seen.append(list(entered)), prefill(*a, **kw))[1])
+    y = Layer(seed=33, B=1)
+    q, k, v = y.qkv(20)
+    out = sk.prefill_paged(q, k, v, i32([0] * 20), i32(range(20)), y.k_pages, y.v_pages, y.table, L=20,
+                           sm_scale=y.scale, threshold_scale_factor=0.0, **y.rope)
+    torch.cuda.synchronize()
+    assert seen == [[q.get_device()]] and out["o"].device == q.device
