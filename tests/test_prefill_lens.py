@@ -196,3 +196,46 @@ def test_prefill_paged_makes_its_tensors_device_current(monkeypatch):
                            sm_scale=y.scale, threshold_scale_factor=0.0, **y.rope)
     torch.cuda.synchronize()
     assert seen == [[q.get_device()]] and out["o"].device == q.device
+
+
+@gpu
+def test_prefill_paged_captured_and_replayed_with_other_lengths():
+    """A graph of a batch's prefill, replayed with prompts of other lengths, and
+    the same call on a stream of its own."""
+    y, L, B = Layer(seed=35, B=3), 200, 3
+    kw = dict(L=L, sm_scale=y.scale, threshold_scale_factor=40.0, **y.rope)
+    pos = torch.arange(L).repeat(B).int().cuda()
+
+    def ids(lens):
+        seq = torch.arange(B).repeat_interleave(L).int()
+        for b, n in enumerate(lens):
+            seq[b * L + n:(b + 1) * L] = -1
+        return seq.cuda()
+
+    q, k, v = (x.contiguous() for x in y.qkv(B * L))
+    seq = ids([200, 130, 1])
+    call = lambda st=None: sk.prefill_paged(q, k, v, seq, pos, y.k_pages, y.v_pages, y.table,  # noqa: E731
+                                            stream=st, **kw)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = call()
+    for lens in ([200, 130, 1], [0, 64, 65], [129, 200, 128]):
+        for x, n in zip((q, k, v), y.qkv(B * L)):
+            x.copy_(n)
+        seq.copy_(ids(lens))
+        g.replay()
+        got = {n: out[n].clone() for n in ("o", "lse", "counts")}
+        side.wait_stream(torch.cuda.current_stream())
+        want = call(side)
+        torch.cuda.synchronize()
+        assert sk.sskip_get_status() == sk.SSKIP_OK
+        for n in got:
+            assert torch.equal(got[n], want[n]), n
+        for b, n in enumerate(lens):
+            assert bool((got["o"][b, :, n:] == 0).all()) and bool(torch.isfinite(got["o"][b].float()).all())
+    del g
