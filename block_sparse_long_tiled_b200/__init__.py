@@ -731,8 +731,10 @@ def paged_cache(num_pages: int, Hkv: int, page_size: int, d: int, *, int4: bool 
 
 
 def paged_splits(B: int, Hkv: int, max_len: int) -> int:
-    """A num_splits that gives every SM four CTAs where the sequences are long
-    enough (a split has at least four tiles of 64 keys)."""
+    """A num_splits that gives every SM four CTAs where sequences of max_len keys
+    are long enough (a split has at least four tiles of 64 keys). A caller that
+    knows its lengths does better: sequences far shorter than max_len leave most
+    splits empty, and up to eight splits merge without a second kernel."""
     return max(1, min(64, -(-592 // max(1, B * Hkv)), -(-max_len // 256)))
 
 

@@ -48,7 +48,7 @@
 // all; then it publishes its tile's maxima, and after the round's one barrier
 // all walk the four tiles in order under the rule (a head a lane).  The barrier
 // also says that the V slots are read, and a kept tile's V is fetched behind it.
-// Factor 500 (63 % skipped), same workload: 368 us; 395 with a kept tile's V
+// Factor 500 (63 % skipped), same workload: 370 us; 395 with a kept tile's V
 // worked on by its own warp, 391 with the barrier ahead of the V work and a
 // second one, 490 with 15 or 16 warps of 136 or 128 registers an SM.
 #pragma once
@@ -190,8 +190,6 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP, DEEP>::kCtas)
                         ((size_t)kvh << shift) * (REC / 16);
   const uint32_t page_bytes = (uint32_t)(p.Hkv << shift) * (REC / 16);
   const uint32_t dst = ((lane & 4) ? vbuf : kbuf) + sub * copy_bytes;
-  // key: this lane's first key of a tile.  Nothing looks at the number before
-  // the copy is issued: the look-up is a trip to memory.
   // key: this lane's first key of a tile.  The number is looked at when its copy
   // is issued, not here: the look-up is a trip to memory.
   auto page_at = [&](int key) { return copies && key < end ? table[key >> shift] : 0; };
@@ -286,7 +284,8 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP, DEEP>::kCtas)
   float acc[MT][4];                // O^T of the codes, in units of 2^-133
   // 8 sum of P', in the same units: a group in an accumulator of its own, the
   // same in every row, or (four groups) group gr in rows 4 gr .. 4 gr + 3 of one,
-  // which saves the registers that made the kernel spill (407 us and 398).
+  // which saves twelve registers of a kernel that has none to spare (407 us and
+  // 398; 24 bytes a thread are spilled all the same).
   constexpr int NE = NG == 4 ? 1 : NG;
   float eight[NE][4];
   // Sum of p (8 sc + mn), or (ZMMA) of p sc and p mn: rows 2 g' and 2 g' + 1 of
@@ -362,6 +361,7 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP, DEEP>::kCtas)
       uint32_t t0, t1;
       ldsm2_t(rec + CODES + (lane & 15) * 16, t0, t1);
       float z[4] = {zacc[0][0], zacc[0][1], zacc[1][0], zacc[1][1]};
+      // (P in bf16 here too; in two parts 411 us for 397.)
       mma16816(z, t0, 0u, t1, 0u, transpose8x8(pack_bf16x2(pr[0], pr[1])),
                transpose8x8(pack_bf16x2(pr[2], pr[3])));
       zacc[0][0] = z[0]; zacc[0][1] = z[1]; zacc[1][0] = z[2]; zacc[1][1] = z[3];
@@ -375,7 +375,11 @@ __global__ void __launch_bounds__(kP4Threads, Paged4Cfg<D, SKIP, DEEP>::kCtas)
         zacc[gr][0] = fmaf(pr[0], za, fmaf(pr[2], zb, zacc[gr][0]));
         zacc[gr][1] = fmaf(pr[1], za, fmaf(pr[3], zb, zacc[gr][1]));
       }
-      // The scale joins P before its rounding to bf16 (2^-8 of the product).
+      // The scale joins P before its rounding to bf16 (2^-8 of the product at
+      // most, where 4 bits leave a value off by a thirtieth of its group's spread).
+      // In two bf16 parts, as over bf16 pages, the calls' error against 64 bits
+      // falls from 1.9 to 1.7 thousandths, O's own rounding, and 64 x 16K-32K takes
+      // 498 us for 397 (factor 500: 404 for 370).
       const uint32_t b0 = transpose8x8(pack_bf16x2(pr[0] * sa, pr[1] * sa));
       const uint32_t b1 = transpose8x8(pack_bf16x2(pr[2] * sb, pr[3] * sb));
       uint32_t a[4], e[4];

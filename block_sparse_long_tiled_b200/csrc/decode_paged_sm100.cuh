@@ -23,8 +23,8 @@
 // maxima (one named barrier a tile), all take the same decision, and the V
 // tile is fetched after it, kLag tiles ahead of its use; a skipped tile costs
 // no V bytes.  64 sequences of 16K-32K (8 kv heads, d = 128): 896 us, 7.2 TB/s,
-// without a threshold; at factor 500 (63 % skipped) 648 us, 6.8 TB/s of what it
-// reads.
+// without a threshold; at factor 500 (63 % skipped) 650 us, 6.8 TB/s of what it
+// reads (699 us where calls on three such caches take turns).
 #pragma once
 
 #include "kvcache_sm100.cuh"

@@ -3,11 +3,11 @@
 // 32 neighbouring values of a row share a scale and a minimum, both bf16:
 //   mn = min rounded down, sc = (max - mn) / 15 rounded up (2^-126 at least, or
 //   0), n = rint((x - mn) / sc)
-// clamped to 0 .. 15, and the value read back is sc n + mn.  Rounding mn down
+// and the value read back is sc n + mn.  n is 0 .. 15 by itself.  Rounding mn down
 // and sc up keeps every value inside [mn, mn + 15 sc], so no value is off by
 // more than sc / 2.  Codes are those of the exact quotient: with the bf16 inputs
-// of the values exact ties are common, and they go to the even code.  A group that holds a NaN or an infinity, or whose spread does
-// not fit, reads back as NaN.
+// of the values exact ties are common, and they go to the even code.  A group
+// that holds a NaN or an infinity, or whose spread does not fit, reads back as NaN.
 //
 // A record is 16 rows of one head: the codes (8 D bytes), then [16][D / 32]
 // pairs (sc, mn).  The code order is the one in which a warp's m16n8k16

@@ -1064,12 +1064,15 @@ SSKIP_API int sskip_kv_append(const sskip_kv_append_args* args, void* stream) {
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool q4 = cached && a.cache.kv_format == SSKIP_KV_INT4;
   // Up to 16 tokens an SM get a CTA each, of as many warps as the SMs hold at
-  // a time (32 query and 8 kv heads, us with 12 / 6 / 4 / 3 warps: 148 tokens 3.0 /
-  // 3.5 / 4.0 / 4.4, 300 5.1 / 4.2 / 4.5 / 5.0, 600 7.0 / 6.3 / 5.3 / 5.6); six
-  // CTAs of four warps fit an SM, so the next two CTAs an SM have three (1000
+  // a time (32 query and 8 kv heads, d = 128, us with 12 / 6 / 4 / 3 warps: 148
+  // tokens 3.0 / 3.5 / 4.0 / 4.4, 300 5.1 / 4.2 / 4.5 / 5.0, 600 7.0 / 6.3 / 5.3 /
+  // 5.6).  At 70 to 79 registers a thread an SM holds six or seven CTAs of four
+  // warps, eight and more of three, so tokens for seven or eight CTAs an SM get
+  // three, in one wave of an even spread (1000
   // tokens 8.1 with four, 6.8 with three; 4-bit 9.8 and 9.1), which loses where
   // there is a second wave anyway (1500 tokens 9.2 and 9.6).  More tokens get a
-  // warp each (16K tokens 75 us, 148 with 12 warps, 94 with 4).
+  // warp each (16K tokens, queries out and the cache filled: 75 us, 148 with 12
+  // warps, 94 with 4).
   const bool alone = T > 16 * 148;
   const int least = T > 6 * 148 && T <= 8 * 148 ? 3 : 4;
   const int warps = std::min(std::min((units + heads - 1) / heads, kAppendMaxWarps),

@@ -412,7 +412,7 @@ int sskip_permute_rows(const void* src, void* dst, const int32_t* idx, long long
  *     bytes, 16 rows each.  32 neighbouring values of a row share
  *       mn = min, rounded down to bf16,   sc = (max - mn) / 15, rounded up to bf16
  *       (a spread above 0 gives at least 2^-126),
- *       n  = rint((x - mn) / sc), ties to even, clamped to 0 .. 15,
+ *       n  = rint((x - mn) / sc), ties to even: 0 .. 15,
  *     and stand for sc n + mn.  A group that holds a NaN or an infinity reads
  *     back as NaN.  The order of the codes, then of the [16][d / 32] bf16
  *     pairs (sc, mn), is the one the decode kernel's tensor-core fragments
@@ -523,8 +523,9 @@ int sskip_kv_append(const sskip_kv_append_args* args, void* stream);
 /*
  * Rows of the cache back as bf16: for T tokens (seq_ids, positions as above;
  * padding and out-of-range tokens leave their rows as they were), keys and
- * values into k_out, v_out [T / out_len, Hkv, out_len, d].  A cached prefix for
- * the prefill, a contiguous cache for sskip_attn_decode, an export.  4-bit
+ * values into k_out, v_out [T / out_len, Hkv, out_len, d].  A contiguous cache for
+ * sskip_attn_decode, an export.  (No prefill attends from new queries alone to
+ * cached keys: its queries and keys have one length.)  4-bit
  * values are computed in fp32 and rounded once to bf16.  The same token may be
  * asked for several times.  The outputs may not overlap each other or anything
  * that the call reads.  T = 0 does nothing.
