@@ -3,10 +3,11 @@
 Thin Python binding of libsskip_attn.so (C ABI in include/sskip_attn.h). The
 sskip_* functions below only marshal torch tensors into the C calls of the
 same names (those of the paged cache through the compiled _binding*.so), and the
-conveniences after them only allocate outputs and chain those calls: every step of the computation runs in the library, in its CUDA
+conveniences after them only allocate outputs, count a batch's tokens and chain
+those calls: every step of the computation runs in the library, in its CUDA
 kernels or, for the host-side steps (the calibration's factor selection, the
-Hilbert order and the rotation frequencies), in its C++. There is no CPU fallback; a missing
-library is an error.
+Hilbert order and the rotation frequencies), in its C++. There is no CPU
+fallback; a missing library is an error.
 
 The method (TensorRT-LLM Skip-Softmax article, "Skip Softmax 的三步走算法"
 section): per attention tile, compare the tile's local maximum logit with the

@@ -597,8 +597,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         }
       }
       // A maximum that keeps a NaN: its row fails the vote, so that the tile is kept
-      // and the NaN reaches the outputs.  Three-input max tree: a first level of independent maxima over column
-      // triples, then levels of three until one value is left.
+      // and the NaN reaches the outputs.  Three-input max tree: a first level of
+      // independent maxima over column triples, then levels of three until one
+      // value is left.
       float t[(BC + 2) / 3];
 #pragma unroll
       for (int i = 0; i < BC / 3; ++i) t[i] = max_nan(s[3 * i], s[3 * i + 1], s[3 * i + 2]);

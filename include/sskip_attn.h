@@ -39,6 +39,9 @@
  *    or index) are latched in a per-device status
  *    word that sskip_get_status() reads.  No C++ exception crosses this ABI.
  *  - Outputs, the counters included, are overwritten, never accumulated.
+ *  - A NaN in a query, or in a key that a row sees, gives NaN in that row's O and
+ *    lse and in no other row's; the tiles it stands in are kept.  A row whose
+ *    scores are all -inf, or that sees no key, gives O = 0 and lse = -inf.
  *  - Debug build.  libsskip_attn_debug.so exports the same functions from the
  *    same sources compiled with device-side checks of tile, ring and record
  *    indices (a stand-in for a memory checker).  A failed check latches
