@@ -293,6 +293,7 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm<D, G>())
         // heads of (m_local - m_run) + ln(L_b) (any factor while t_b < 1).
         float gap = (m_loc == -INFINITY) ? -INFINITY
                     : (m_run == -INFINITY) ? INFINITY : m_loc - m_run;
+        if (gap != gap) gap = INFINITY;  // NaN: no factor skips the tile
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) gap = fmaxf(gap, __shfl_xor_sync(0xffffffffu, gap, o));
         if (lane == 0 && dev_check(j0 + t < p.n_k_max))

@@ -624,6 +624,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         // Largest gap m_local - m_run over the warp's valid rows (log2 units).
         float gap = (!(row_in && gvis) || m_loc == -INFINITY) ? -INFINITY
                     : (m_run == -INFINITY) ? INFINITY : m_loc - m_run;
+        if (gap != gap) gap = INFINITY;  // NaN: no factor skips the tile
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) gap = fmaxf(gap, __shfl_xor_sync(0xffffffffu, gap, o));
         if (lane == 0) wgap[fs + wq] = gap;

@@ -168,3 +168,33 @@ def test_contiguous_decode_of_nan(Hq, d, splits, tsf):
     assert bool(got["o"][1, :G].isnan().all()) and bool(got["lse"][1, :G].isnan().all())
     assert torch.equal(got["o"][1, G:], clean["o"][1, G:])
     assert bool(torch.isfinite(got["o"][[0, 2, 3]].float()).all())
+
+
+@pytest.mark.parametrize("tsf", [0.0, 20.0])
+def test_no_factor_skips_a_tile_of_nan(tsf):
+    """The critical values: +inf for every tile of the rows that a NaN query
+    makes its query tile keep, and the call's own decisions follow the record."""
+    L = 384
+    q, k, v = inputs(1, 2, 1, L, 64)
+    q[0, 0, 200] = float("nan")
+    o, lse = torch.empty_like(q), torch.empty(1, 2, L, device="cuda")
+    crit = torch.empty(1, 2, 3, 3, device="cuda")
+    state = torch.empty(1, 2, 3, 3, device="cuda", dtype=torch.uint8)
+    sk.sskip_attn_prefill_vote(q, k, v, o, lse, causal=True, sm_scale=0.125, threshold_scale_factor=tsf,
+                               vote_rows=128, tile_state=state, tile_crit=crit)
+    torch.cuda.synchronize()
+    assert crit[0, 0, 1, :2].tolist() == [float("inf")] * 2 and state[0, 0, 1, :2].tolist() == [1, 1]
+    assert bool(torch.isfinite(crit[0, 1, 1, 1]))  # the other head's
+    if tsf:
+        seen = state > 0
+        assert torch.equal(state[seen] == 2, crit[seen] < torch.tensor(tsf, device="cuda").log())
+    lens = torch.tensor([L], dtype=torch.int32, device="cuda")
+    qd = q[:, :, 200].contiguous()
+    crit = torch.empty(1, 1, 6, device="cuda")
+    state = torch.empty(1, 1, 6, device="cuda", dtype=torch.uint8)
+    ws = torch.empty(sk.sskip_attn_decode_workspace_size(1, 2, 64, 2), device="cuda", dtype=torch.uint8)
+    sk.sskip_attn_decode_crit(qd, k, v, lens, torch.empty_like(qd), torch.empty(1, 2, device="cuda"),
+                              sm_scale=0.125, threshold_scale_factor=tsf, num_splits=2, workspace=ws,
+                              tile_state=state, tile_crit=crit)
+    torch.cuda.synchronize()
+    assert crit.flatten().tolist() == [float("inf")] * 6 and state.flatten().tolist() == [1] * 6
