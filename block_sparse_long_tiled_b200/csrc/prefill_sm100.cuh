@@ -545,10 +545,14 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     const int grp = r / BR;
     const int row = row0 + 128 * wg + r;
     const bool row_in = row < L;
-    // The first key that the row does not see: one number to mask by, not L and
-    // the row (16K causal, d = 128: 2001 us with two, 1970 with one; with LENS,
-    // where L is a register, 2083 and 2011).
+    // The first key that the row does not see: one number to mask by, not the length
+    // and the row (16K causal, d = 128: 2001 us with two, 1970 with one; with LENS,
+    // where the length is a register, 2083 and 2011; EXT at d = 64 1863 and 1751).
+    // EXT at d = 128 has no register for it (2160 us with two, 2255 with one).
     const int end = CAUSAL ? min(L, row + 1) : L;
+    auto hidden = [&](int key) {
+      return EXT && D == 128 ? key >= L || (CAUSAL && key > row) : key >= end;
+    };
     const uint32_t lane_base = uint32_t(wq * 32) << 16;
     const uint32_t tO = tmem + C::kOCol + wg * D + lane_base;
     const int n_own = wg == 0 ? n_a : n_b;
@@ -588,12 +592,12 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 
       // Mask: keys past the length, and keys after the row in causal attention.
       const int key0 = j * BC;
-      const bool need_mask = key0 + BC > end;
+      const bool need_mask = hidden(key0 + BC - 1);
       if (need_mask) {
 #pragma unroll
         for (int c = 0; c < BC; ++c) {
           const int key = key0 + c;
-          if (key >= end) s[c] = -INFINITY;
+          if (hidden(key)) s[c] = -INFINITY;
         }
       }
       // A maximum that keeps a NaN: its row fails the vote, so that the tile is kept
@@ -760,7 +764,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 #pragma unroll
           for (int c = 0; c < HK; ++c) {
             const int key = key0 + HK + c;
-            if (key >= end) rr[c] = __float_as_uint(-INFINITY);
+            if (hidden(key)) rr[c] = __float_as_uint(-INFINITY);
           }
         }
         exp_half(1, reinterpret_cast<const float*>(rr));
